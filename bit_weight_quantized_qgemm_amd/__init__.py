@@ -19,7 +19,8 @@ __all__ = [
     "w4a8_fp16", "FMT_W4G", "DT_F16", "DT_BF16", "packed_bytes_w4g", "workspace_bytes_w4g",
     "repack_w4g", "w4g", "FMT_W4A16_SP24", "repack_sp24", "w4a16_sp24", "FMT_BITPLANE",
     "packed_bytes_bitplane", "workspace_bytes_bitplane", "repack_bitplane", "bitplane_a8", "plan_info",
-    "w4a16_noalloc",
+    "w4a16_noalloc", "DT_FP8", "KVCache", "rope_table", "qk_rope_append", "attn_decode", "attn_prefill",
+    "set_attn_splits", "attn_decode_workspace_bytes", "attn_prefill_workspace_bytes",
 ]
 
 FMT_W4A16 = 1
@@ -30,6 +31,7 @@ FMT_W4A16_SP24 = 5
 FMT_BITPLANE = 6
 DT_F16 = 1
 DT_BF16 = 2
+DT_FP8 = 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # QGEMM_LIB selects another build of the same library (the host-sanitized
@@ -44,6 +46,8 @@ EXPORTED_SYMBOLS = (
     "qgemm_w4g_workspace_bytes", "qgemm_w4g_repack", "qgemm_w4g", "qgemm_w4a16_sp24",
     "qgemm_bitplane_packed_bytes", "qgemm_bitplane_workspace_bytes", "qgemm_bitplane_repack",
     "qgemm_bitplane_a8", "qgemm_bitplane_plan", "qgemm_w4g_plan", "qgemm_plan_info", "qgemm_w4a16_noalloc",
+    "qgemm_qk_rope_append", "qgemm_attn_decode_workspace_bytes", "qgemm_attn_decode",
+    "qgemm_attn_prefill_workspace_bytes", "qgemm_attn_prefill", "qgemm_attn_set_splits",
 )
 
 
@@ -94,7 +98,19 @@ def lib() -> ctypes.CDLL:
         L.qgemm_plan_info.argtypes = [ctypes.c_int, i64, i64, i64, i32, i32, i32, i32,
                                       ctypes.POINTER(ctypes.c_int64)]
         L.qgemm_w4a16_noalloc.argtypes = [vp, i64, vp, vp, i64, i64, i64, i64, vp]
-        for name in ("qgemm_packed_bytes", "qgemm_workspace_bytes", "qgemm_repack", "qgemm_w4a16",
+        f32 = ctypes.c_float
+        L.qgemm_qk_rope_append.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, f32, vp, i64, i32, i32, vp,
+                                           vp, vp, i64, i64, i64, i32, i32, vp, vp, i64, i64, vp]
+        L.qgemm_attn_decode_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i32, u64p]
+        L.qgemm_attn_decode.argtypes = [vp, i64, i64, vp, vp, i64, vp, i64, i64, i32, i32, f32, i64, i32, vp, i64, i64,
+                                        vp, ctypes.c_size_t, vp]
+        L.qgemm_attn_prefill_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i64, i32, u64p]
+        L.qgemm_attn_prefill.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, i32, f32, i64, i32,
+                                         vp, i64, i64, vp, ctypes.c_size_t, vp]
+        L.qgemm_attn_set_splits.argtypes = [ctypes.c_int]
+        for name in ("qgemm_qk_rope_append", "qgemm_attn_decode_workspace_bytes", "qgemm_attn_decode",
+                     "qgemm_attn_prefill_workspace_bytes", "qgemm_attn_prefill", "qgemm_attn_set_splits",
+                     "qgemm_packed_bytes", "qgemm_workspace_bytes", "qgemm_repack", "qgemm_w4a16",
                      "qgemm_w4a8", "qgemm_w2w4_mixed", "qgemm_plan", "qgemm_set_plan_override",
                      "qgemm_quantize_a8", "qgemm_w4g_packed_bytes", "qgemm_w4g_workspace_bytes",
                      "qgemm_w4g_repack", "qgemm_w4g", "qgemm_w4a16_sp24", "qgemm_bitplane_packed_bytes",
@@ -439,3 +455,8 @@ def bitplane_a8(A_i8, a_scale, blob, K: int, N: int, bits: int, out=None, acc_ou
                                    out.stride(0), _ptr(acc_out), M, K, N, bits, _ptr(ws), wsb,
                                    _stream_ptr(A_i8.device)), "qgemm_bitplane_a8")
     return out
+
+
+# ----------------------------------------------------------------------------- attention
+from .attention import (KVCache, attn_decode, attn_decode_workspace_bytes, attn_prefill,  # noqa: E402
+                        attn_prefill_workspace_bytes, qk_rope_append, rope_table, set_attn_splits)

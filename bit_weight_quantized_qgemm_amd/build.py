@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libqgemm.so")
 PROBES_LIB = os.path.join(HERE, "libqgemm_probes.so")
 PROBES_SOURCES = ["probes.hip"]
 SOURCES = ["api.cpp", "repack.hip", "w4a16.hip", "w4a8.hip", "w2w4.hip", "wide.hip", "quant.hip", "w4g.hip", "sp24.hip",
-           "bitplane_lo.hip", "bitplane_hi.hip", "noalloc.hip"]
+           "bitplane_lo.hip", "bitplane_hi.hip", "noalloc.hip", "attn_api.cpp", "rope_append.hip", "attn_decode.hip",
+           "attn_prefill.hip"]
 ARCH = "gfx950"
 
 

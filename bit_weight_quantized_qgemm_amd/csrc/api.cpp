@@ -877,6 +877,8 @@ namespace qg {
 
 int fail_hip(hipError_t e, const char* what) { return hip_fail(e, what); }
 
+int check_current_device() { return check_device(); }
+
 void set_last_error(const std::string& text) { g_last_error = text; }
 
 int validate_w4a16(const void* A, int64_t lda, const void* packed, void* C, int64_t ldc, int64_t M, int64_t K,

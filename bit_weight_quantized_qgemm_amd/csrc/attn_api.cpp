@@ -1,0 +1,424 @@
+// C-ABI front end of the attention operators: argument validation (before any
+// HIP call), the split of the cache's length and kernel dispatch. See
+// include/qgemm.h for the contract.
+#include "qgemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_internal.h"
+
+namespace {
+
+constexpr int64_t kMaxSeqs = 65535;
+constexpr int64_t kMaxTokens = int64_t(1) << 20;
+constexpr int64_t kMaxLen = int64_t(1) << 24;
+constexpr int kMaxKvHeads = 1024;
+constexpr int kMaxGroup = 128;
+constexpr int kMaxHeadDim = 256;
+constexpr int64_t kMaxTokenStride = int64_t(1) << 25;
+
+std::atomic<int> g_force_splits{0};
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool valid_act(int dt) { return dt == QGEMM_DT_F16 || dt == QGEMM_DT_BF16; }
+
+bool positive(float x) { return std::isfinite(x) && x > 0.f; }
+
+// A tensor's bytes in memory: [first, last).
+struct Extent {
+  uintptr_t first = 0, last = 0;
+};
+
+bool overlap(const Extent& a, const Extent& b) { return a.first < b.last && b.first < a.last; }
+
+Extent extent(const void* p, int64_t elems, int64_t elt) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return p && elems > 0 ? Extent{a, a + (uintptr_t)(elems * elt)} : Extent{};
+}
+
+// [tokens][heads][dim] with the given strides
+Extent extent3(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t dim) {
+  return extent(p, (tokens - 1) * ts + (heads - 1) * hs + dim, 2);
+}
+
+// Strides of a [tokens][heads][dim] tensor: 16-byte rows that do not overlap
+// within a token; bounded so that no extent overflows.
+bool valid_strides(int64_t ts, int64_t hs, int64_t heads, int64_t dim) {
+  constexpr int64_t kMost = int64_t(1) << 32;
+  return ts >= 0 && hs >= 0 && ts <= kMost && hs <= kMost && ts % 8 == 0 && hs % 8 == 0 && (heads == 1 || hs >= dim);
+}
+// ... of one that is written: its tokens must not overlap either.
+bool valid_out_strides(int64_t tokens, int64_t ts, int64_t hs, int64_t heads, int64_t dim) {
+  return valid_strides(ts, hs, heads, dim) &&
+         (tokens == 1 || ts >= (heads - 1) * hs + dim || (ts >= dim && hs >= (tokens - 1) * ts + dim));
+}
+
+int check_cache(const qgemm_kv_cache* c, int act_dtype) {
+  if (c->kv_heads < 1 || c->kv_heads > kMaxKvHeads) return QGEMM_ERR_SHAPE;
+  if (c->head_dim < 16 || c->head_dim > kMaxHeadDim || c->head_dim % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (c->num_pages < 1 || c->num_pages > INT32_MAX) return QGEMM_ERR_SHAPE;
+  if (c->dtype != QGEMM_DT_F16 && c->dtype != QGEMM_DT_BF16 && c->dtype != QGEMM_DT_FP8) return QGEMM_ERR_RANGE;
+  if (c->dtype != QGEMM_DT_FP8 && c->dtype != act_dtype) return QGEMM_ERR_RANGE;
+  if (!positive(c->k_scale) || !positive(c->v_scale)) return QGEMM_ERR_RANGE;
+  if (c->dtype != QGEMM_DT_FP8 && (c->k_scale != 1.f || c->v_scale != 1.f)) return QGEMM_ERR_RANGE;
+  if (!c->k || !c->v) return QGEMM_ERR_NULL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QGEMM_ERR_ALIGN;
+  const int64_t step = c->dtype == QGEMM_DT_FP8 ? 16 : 8;
+  constexpr int64_t kMost = int64_t(1) << 40;
+  if (c->token_stride < c->head_dim || c->token_stride > kMaxTokenStride || c->token_stride % step != 0)
+    return QGEMM_ERR_ALIGN;
+  if (c->head_stride < 0 || c->head_stride > kMost || c->head_stride % step != 0 ||
+      (c->kv_heads > 1 && c->head_stride < c->head_dim))
+    return QGEMM_ERR_ALIGN;
+  // 2^31 pages of 2^30 elements stay below 2^62
+  if (c->page_stride < 0 || c->page_stride > (int64_t(1) << 30) || c->page_stride % step != 0) return QGEMM_ERR_ALIGN;
+  return QGEMM_OK;
+}
+
+Extent cache_extent(const qgemm_kv_cache* c, const void* p) {
+  const int64_t elems = (c->num_pages - 1) * c->page_stride + (c->page_size - 1) * c->token_stride +
+                        (c->kv_heads - 1) * c->head_stride + c->head_dim;
+  return extent(p, elems, c->dtype == QGEMM_DT_FP8 ? 1 : 2);
+}
+
+qg::CacheArgs cache_args(const qgemm_kv_cache* c, const int32_t* table, int64_t table_stride) {
+  qg::CacheArgs a{};
+  a.k = c->k;
+  a.v = c->v;
+  a.page_stride = c->page_stride;
+  a.token_stride = c->token_stride;
+  a.head_stride = c->head_stride;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.num_pages = (int32_t)c->num_pages;
+  a.page_blocks = c->page_size / qg::kTokBlock;
+  const uint64_t d = (uint64_t)a.page_blocks;
+  a.magic = d == 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + d - 1) / d);
+  return a;
+}
+
+int check_heads(int32_t q_heads, int32_t kv_heads) {
+  if (q_heads < 1 || q_heads % kv_heads != 0 || q_heads / kv_heads > kMaxGroup) return QGEMM_ERR_SHAPE;
+  return QGEMM_OK;
+}
+
+// Most token blocks that a sequence has to visit.
+int64_t visible_blocks(int64_t max_len, int64_t rows, int64_t window, int32_t sinks) {
+  const int64_t all = (max_len + qg::kTokBlock - 1) / qg::kTokBlock;
+  if (window == 0) return all;
+  return std::min(all, (sinks + qg::kTokBlock - 1) / qg::kTokBlock + (window + rows - 1 + 2 * qg::kTokBlock - 2) / qg::kTokBlock);
+}
+
+void split(qg::AttnPlan& pl, int64_t blocks, int64_t want, int step, int head_dim) {
+  const int force = g_force_splits.load();
+  int64_t splits = force ? force : std::max<int64_t>(1, want);
+  // more tiles than the workspace has counters fill the device without a split
+  if (pl.tiles > qg::kMaxCounters) splits = 1;
+  blocks = std::max<int64_t>(1, blocks);
+  const int64_t per = (blocks + splits - 1) / splits;
+  pl.split_blocks = (int)((per + step - 1) / step * step);
+  pl.splits = (int)((blocks + pl.split_blocks - 1) / pl.split_blocks);
+  pl.ws_bytes = 0;
+  if (pl.splits > 1) {
+    const size_t parts = (size_t)pl.tiles * pl.splits;
+    pl.stats_offset = qg::kCounterBytes;
+    pl.partial_offset = pl.stats_offset + qg::align256(parts * pl.part_rows * 8);
+    pl.ws_bytes = pl.partial_offset + parts * pl.part_rows * head_dim * 4;
+  }
+}
+
+qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_heads, int head_dim, int64_t window,
+                         int32_t sinks) {
+  qg::AttnPlan pl;
+  const int group = q_heads / kv_heads;
+  pl.row_tiles = (group + qg::kDecodeRows - 1) / qg::kDecodeRows;
+  pl.part_rows = std::min(group, qg::kDecodeRows);
+  pl.tiles = num_seqs * kv_heads * pl.row_tiles;
+  const int64_t blocks = visible_blocks(max_len, 1, window, sinks);
+  constexpr int kStep = 2 * qg::kDecodeWaves;   // one pair of blocks for each wave
+  const int64_t fill = 4 * (int64_t)qg::device_cu_count();
+  split(pl, blocks, std::min(fill / pl.tiles, (blocks + kStep - 1) / kStep), kStep, head_dim);
+  return pl;
+}
+
+qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int q_heads, int kv_heads, int head_dim,
+                          int64_t window, int32_t sinks) {
+  qg::AttnPlan pl;
+  const int64_t rows = max_q * (q_heads / kv_heads);
+  pl.row_tiles = (int)((rows + qg::kPrefillRows - 1) / qg::kPrefillRows);
+  pl.part_rows = (int)std::min<int64_t>(rows, qg::kPrefillRows);
+  pl.tiles = num_seqs * kv_heads * pl.row_tiles;
+  const int64_t blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), window, sinks);
+  constexpr int kStep = 4;   // blocks of a tile of K and V
+  const int64_t fill = 2 * (int64_t)qg::device_cu_count();
+  split(pl, blocks, std::min(fill / pl.tiles, (blocks + kStep - 1) / kStep), kStep, head_dim);
+  return pl;
+}
+
+int check_attn_shape(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                     int64_t window, int32_t sinks) {
+  if (num_seqs < 0 || num_seqs > kMaxSeqs) return QGEMM_ERR_SHAPE;
+  if (max_len < 0 || max_len > kMaxLen) return QGEMM_ERR_SHAPE;
+  if (kv_heads < 1 || kv_heads > kMaxKvHeads) return QGEMM_ERR_SHAPE;
+  if (head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (window < 0 || sinks < 0) return QGEMM_ERR_RANGE;
+  return check_heads(q_heads, kv_heads);
+}
+
+struct AttnCall {
+  const void* q;
+  int64_t q_ts, q_hs;
+  const qgemm_kv_cache* cache;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* q_start;   // prefill only
+  const int32_t* lens;
+  int64_t num_seqs, num_tokens, max_q, max_len;
+  int32_t q_heads, act_dtype;
+  float scale;
+  int64_t window;
+  int32_t sinks;
+  void* out;
+  int64_t o_ts, o_hs;
+  void* ws;
+  size_t ws_bytes;
+  void* stream;
+  bool prefill;
+};
+
+int run_attn(const AttnCall& g) {
+  const qgemm_kv_cache* c = g.cache;
+  if (!c) return QGEMM_ERR_NULL;
+  if (!valid_act(g.act_dtype)) return QGEMM_ERR_RANGE;
+  int st = check_attn_shape(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
+  if (st) return st;
+  if (g.num_tokens < 0 || g.num_tokens > kMaxTokens || g.max_q < 0 || g.max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
+  st = check_cache(c, g.act_dtype);
+  if (st) return st;
+  if (!positive(g.scale) || !positive(g.scale * c->k_scale)) return QGEMM_ERR_RANGE;
+  if (g.num_seqs == 0 || g.num_tokens == 0 || g.max_q == 0) return QGEMM_OK;
+  if (!g.q || !g.out || !g.lens || (!g.table && g.table_stride > 0) || (g.prefill && !g.q_start)) return QGEMM_ERR_NULL;
+  if (!aligned(g.q, 16) || !aligned(g.out, 16) || !aligned(g.lens, 4) || !aligned(g.table, 4) || !aligned(g.q_start, 4))
+    return QGEMM_ERR_ALIGN;
+  if (!valid_strides(g.q_ts, g.q_hs, g.q_heads, c->head_dim) ||
+      !valid_out_strides(g.num_tokens, g.o_ts, g.o_hs, g.q_heads, c->head_dim))
+    return QGEMM_ERR_ALIGN;
+  if (g.table_stride < 0 || g.table_stride > kMaxLen || g.max_len > g.table_stride * c->page_size)
+    return QGEMM_ERR_SHAPE;
+
+  const qg::AttnPlan pl =
+      g.prefill ? prefill_plan(g.num_seqs, g.max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks)
+                : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
+  if (pl.tiles * pl.splits > INT32_MAX) return QGEMM_ERR_SHAPE;
+  if (pl.ws_bytes > 0) {
+    if (!g.ws) return QGEMM_ERR_NULL;
+    if (g.ws_bytes < pl.ws_bytes) return QGEMM_ERR_WORKSPACE;
+    if (!aligned(g.ws, 16)) return QGEMM_ERR_ALIGN;
+  }
+  const Extent out = extent3(g.out, g.num_tokens, g.o_ts, g.q_heads, g.o_hs, c->head_dim);
+  const Extent others[] = {extent3(g.q, g.num_tokens, g.q_ts, g.q_heads, g.q_hs, c->head_dim),
+                           cache_extent(c, c->k),
+                           cache_extent(c, c->v),
+                           extent(g.table, g.num_seqs * g.table_stride, 4),
+                           extent(g.lens, g.num_seqs, 4),
+                           extent(g.q_start, g.num_seqs + 1, 4),
+                           extent(pl.ws_bytes ? g.ws : nullptr, (int64_t)pl.ws_bytes, 1)};
+  for (const Extent& e : others)
+    if (overlap(out, e)) return QGEMM_ERR_ALIAS;
+  if (pl.ws_bytes)
+    for (const Extent& e : others)
+      if (&e != &others[6] && overlap(others[6], e)) return QGEMM_ERR_ALIAS;
+  st = qg::check_current_device();
+  if (st) return st;
+
+  qg::AttnArgs a{};
+  a.q = g.q;
+  a.out = g.out;
+  a.q_ts = g.q_ts;
+  a.q_hs = g.q_hs;
+  a.o_ts = g.o_ts;
+  a.o_hs = g.o_hs;
+  a.cache = cache_args(c, g.table, g.table_stride);
+  a.lens = g.lens;
+  a.q_start = g.q_start;
+  a.num_seqs = (int32_t)g.num_seqs;
+  a.kv_heads = c->kv_heads;
+  a.group = g.q_heads / c->kv_heads;
+  a.head_dim = c->head_dim;
+  a.num_tokens = (int32_t)g.num_tokens;
+  a.max_q = (int32_t)g.max_q;
+  a.max_len = (int32_t)g.max_len;
+  // a window beyond every position is none; sinks beyond max_len are all tokens
+  a.window = g.window >= g.max_len ? 0 : (int32_t)g.window;
+  a.sinks = (int32_t)std::min<int64_t>(g.sinks, g.max_len);
+  a.row_tiles = pl.row_tiles;
+  a.part_rows = pl.part_rows;
+  a.splits = pl.splits;
+  a.split_blocks = pl.split_blocks;
+  a.scale_log2 = g.scale * c->k_scale * 1.44269504088896340736f;
+  a.v_scale = c->v_scale;
+  if (pl.ws_bytes) {
+    char* ws = static_cast<char*>(g.ws);
+    a.counters = reinterpret_cast<uint32_t*>(ws);
+    a.stats = reinterpret_cast<float*>(ws + pl.stats_offset);
+    a.partial = reinterpret_cast<float*>(ws + pl.partial_offset);
+  }
+  const bool bf16 = g.act_dtype == QGEMM_DT_BF16, fp8 = c->dtype == QGEMM_DT_FP8;
+  hipStream_t s = static_cast<hipStream_t>(g.stream);
+  const hipError_t e = g.prefill ? qg::launch_attn_prefill(a, bf16, fp8, pl.tiles, s)
+                                 : qg::launch_attn_decode(a, bf16, fp8, pl.tiles, s);
+  if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
+  return QGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                         int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                         int64_t v_head_stride, const void* q_norm, const void* k_norm, float eps, const float* rope,
+                         int64_t rope_rows, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                         const int32_t* token_seq, const int32_t* block_table, int64_t table_stride, int64_t num_seqs,
+                         int64_t num_tokens, int32_t q_heads, int32_t act_dtype, const qgemm_kv_cache* cache,
+                         void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, void* stream) {
+  const qgemm_kv_cache* c = cache;
+  if (!c) return QGEMM_ERR_NULL;
+  if (!valid_act(act_dtype) || (interleaved != 0 && interleaved != 1)) return QGEMM_ERR_RANGE;
+  if (num_seqs < 0 || num_seqs > kMaxSeqs || num_tokens < 0 || num_tokens > kMaxTokens) return QGEMM_ERR_SHAPE;
+  int st = check_cache(c, act_dtype);
+  if (st) return st;
+  st = check_heads(q_heads, c->kv_heads);
+  if (st) return st;
+  // 32-bit task numbers over the tokens' heads
+  const int64_t heads = (int64_t)q_heads + 2 * c->kv_heads;
+  if (num_tokens * heads >= (int64_t(1) << 31)) return QGEMM_ERR_SHAPE;
+  if (rot_dim < 0 || rot_dim > c->head_dim || rot_dim % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (rope_rows < 0 || rope_rows > kMaxLen) return QGEMM_ERR_SHAPE;
+  if (table_stride < 0 || table_stride > kMaxLen) return QGEMM_ERR_SHAPE;
+  if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.f)) return QGEMM_ERR_RANGE;
+  if (num_tokens == 0) return QGEMM_OK;
+  if (!q || !k || !v || !q_out || !positions || !block_table || (rot_dim > 0 && !rope)) return QGEMM_ERR_NULL;
+  for (const void* p : {q, k, v, q_norm, k_norm, (const void*)rope, (const void*)q_out})
+    if (!aligned(p, 16)) return QGEMM_ERR_ALIGN;
+  if (!aligned(positions, 4) || !aligned(token_seq, 4) || !aligned(block_table, 4)) return QGEMM_ERR_ALIGN;
+  if (!valid_strides(q_token_stride, q_head_stride, q_heads, c->head_dim) ||
+      !valid_strides(k_token_stride, k_head_stride, c->kv_heads, c->head_dim) ||
+      !valid_strides(v_token_stride, v_head_stride, c->kv_heads, c->head_dim) ||
+      !valid_out_strides(num_tokens, qo_token_stride, qo_head_stride, q_heads, c->head_dim))
+    return QGEMM_ERR_ALIGN;
+  const int64_t D = c->head_dim;
+  const Extent eq = extent3(q, num_tokens, q_token_stride, q_heads, q_head_stride, D);
+  const Extent out = extent3(q_out, num_tokens, qo_token_stride, q_heads, qo_head_stride, D);
+  const Extent kc = cache_extent(c, c->k), vc = cache_extent(c, c->v);
+  const Extent in[] = {extent3(k, num_tokens, k_token_stride, c->kv_heads, k_head_stride, D),
+                       extent3(v, num_tokens, v_token_stride, c->kv_heads, v_head_stride, D),
+                       extent(q_norm, D, 2),
+                       extent(k_norm, D, 2),
+                       extent(rope, rope_rows * rot_dim, 4),
+                       extent(positions, num_tokens, 4),
+                       extent(token_seq, num_tokens, 4),
+                       extent(block_table, num_seqs * table_stride, 4)};
+  const bool in_place = q_out == q && qo_token_stride == q_token_stride && qo_head_stride == q_head_stride;
+  if (!in_place && overlap(out, eq)) return QGEMM_ERR_ALIAS;
+  // the parts of one fused product interleave in memory: an in-place q_out may
+  // span k and v without touching them, so only a separate q_out is checked
+  for (const Extent& e : in)
+    if ((!in_place && overlap(out, e)) || overlap(kc, e) || overlap(vc, e)) return QGEMM_ERR_ALIAS;
+  if (overlap(kc, eq) || overlap(vc, eq) || overlap(kc, out) || overlap(vc, out)) return QGEMM_ERR_ALIAS;
+  st = qg::check_current_device();
+  if (st) return st;
+
+  qg::AppendArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.k_ts = k_token_stride;
+  a.k_hs = k_head_stride;
+  a.v_ts = v_token_stride;
+  a.v_hs = v_head_stride;
+  a.qo_ts = qo_token_stride;
+  a.qo_hs = qo_head_stride;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.eps = eps;
+  a.inv_dim = 1.0f / (float)c->head_dim;
+  a.rope = rope;
+  a.rope_rows = rope_rows;
+  a.rot_dim = rot_dim;
+  a.positions = positions;
+  a.token_seq = token_seq;
+  a.cache = cache_args(c, block_table, table_stride);
+  a.num_seqs = (int32_t)num_seqs;
+  a.num_tokens = (int32_t)num_tokens;
+  a.q_heads = q_heads;
+  a.kv_heads = c->kv_heads;
+  a.head_dim = c->head_dim;
+  a.q_out = q_out;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  const hipError_t e = qg::launch_append(a, act_dtype == QGEMM_DT_BF16, c->dtype == QGEMM_DT_FP8, interleaved != 0,
+                                         static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
+  return QGEMM_OK;
+}
+
+int qgemm_attn_decode_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t kv_heads,
+                                      int32_t head_dim, int64_t window, int32_t sinks, size_t* bytes) {
+  if (!bytes) return QGEMM_ERR_NULL;
+  const int st = check_attn_shape(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks);
+  if (st) return st;
+  *bytes = num_seqs == 0 ? 0 : decode_plan(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks).ws_bytes;
+  return QGEMM_OK;
+}
+
+int qgemm_attn_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, const qgemm_kv_cache* cache,
+                      const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, int64_t num_seqs,
+                      int64_t max_len, int32_t q_heads, int32_t act_dtype, float scale, int64_t window, int32_t sinks,
+                      void* out, int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  return run_attn({q, q_token_stride, q_head_stride, cache, block_table, table_stride, nullptr, seq_lens, num_seqs,
+                   num_seqs, 1, max_len, q_heads, act_dtype, scale, window, sinks, out, out_token_stride,
+                   out_head_stride, workspace, workspace_bytes, stream, false});
+}
+
+int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t max_len, int32_t q_heads,
+                                       int32_t kv_heads, int32_t head_dim, int64_t window, int32_t sinks,
+                                       size_t* bytes) {
+  if (!bytes) return QGEMM_ERR_NULL;
+  const int st = check_attn_shape(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks);
+  if (st) return st;
+  if (max_q < 0 || max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
+  *bytes = num_seqs == 0 || max_q == 0
+               ? 0
+               : prefill_plan(num_seqs, max_q, max_len, q_heads, kv_heads, head_dim, window, sinks).ws_bytes;
+  return QGEMM_OK;
+}
+
+int qgemm_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const qgemm_kv_cache* cache,
+                       const int32_t* block_table, int64_t table_stride, const int32_t* q_start,
+                       const int32_t* seq_lens, int64_t num_seqs, int64_t num_tokens, int64_t max_q, int64_t max_len,
+                       int32_t q_heads, int32_t act_dtype, float scale, int64_t window, int32_t sinks, void* out,
+                       int64_t out_token_stride, int64_t out_head_stride, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  return run_attn({q, q_token_stride, q_head_stride, cache, block_table, table_stride, q_start, seq_lens, num_seqs,
+                   num_tokens, max_q, max_len, q_heads, act_dtype, scale, window, sinks, out, out_token_stride,
+                   out_head_stride, workspace, workspace_bytes, stream, true});
+}
+
+int qgemm_attn_set_splits(int splits) {
+  if (splits < 0 || splits > qg::kMaxAttnSplits) return QGEMM_ERR_RANGE;
+  g_force_splits.store(splits);
+  return QGEMM_OK;
+}
+
+}  // extern "C"

@@ -122,4 +122,17 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t expected
   return last;
 }
 
+// Returns true in every thread of the workgroup that arrived last.
+__device__ __forceinline__ bool workgroup_arrive_last(uint32_t* counter, uint32_t total, int* flag) {
+  __builtin_amdgcn_s_waitcnt(0);   // this thread's partial stores are complete
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t prev = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = prev == total - 1;
+    if (prev == total - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *flag != 0;
+}
+
 }  // namespace qg

@@ -142,6 +142,7 @@ hipError_t launch_zero_fill(void* dst, size_t bytes, hipStream_t s);
 // a HIP failure (returns QGEMM_ERR_HIP), record an error text, and run every
 // check of qgemm_w4a16 except the workspace's without launching anything.
 int fail_hip(hipError_t e, const char* what);
+int check_current_device();   // QGEMM_OK on a gfx950 GPU
 void set_last_error(const std::string& text);
 int validate_w4a16(const void* A, int64_t lda, const void* packed, void* C, int64_t ldc, int64_t M, int64_t K,
                    int64_t N);

@@ -86,19 +86,6 @@ __device__ __forceinline__ TileIndex tile_of_block(const GemmArgs& p) {
   return TileIndex{g % p.nt, r, g / p.nt};
 }
 
-// Returns true in every thread of the workgroup that arrived last.
-__device__ __forceinline__ bool workgroup_arrive_last(uint32_t* counter, uint32_t total, int* flag) {
-  __builtin_amdgcn_s_waitcnt(0);   // this thread's partial stores are complete
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint32_t prev = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *flag = prev == total - 1;
-    if (prev == total - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  return *flag != 0;
-}
-
 // Direct buffer-to-LDS copy of `pieces` 16-byte pieces to dst .. dst + 16*pieces
 // (dst 16-byte aligned): piece p comes from byte offset src_of(p) of resource
 // r. The workgroup's waves take 1 KB rows of the destination in turn; lanes

@@ -87,10 +87,12 @@ typedef enum qgemm_fmt {
   QGEMM_FMT_BITPLANE = 6  /* bit-plane W_b A8: only through the qgemm_bitplane_* entry points */
 } qgemm_fmt;
 
-/* Activation (and scale, output) type of the general-grid 4-bit GEMM. */
+/* Activation (and scale, output) type of the general-grid 4-bit GEMM and of the
+ * attention operators. */
 typedef enum qgemm_dtype {
   QGEMM_DT_F16 = 1,   /* IEEE binary16 */
-  QGEMM_DT_BF16 = 2   /* bfloat16 (upper half of binary32) */
+  QGEMM_DT_BF16 = 2,  /* bfloat16 (upper half of binary32) */
+  QGEMM_DT_FP8 = 3    /* e4m3 (OCP: no infinities, largest value 448): key-value caches only */
 } qgemm_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -304,6 +306,141 @@ int qgemm_bitplane_a8(const void* A, int64_t lda, const void* a_scale, const voi
  */
 int qgemm_w4a16_noalloc(const void* A, int64_t lda, const void* packed, void* C, int64_t ldc, int64_t M,
                         int64_t K, int64_t N, void* stream);
+
+/*
+ * Attention around a paged key-value cache: the operators of a decoder layer
+ * between its q/k/v product and its output product (both quantized GEMMs above).
+ *
+ * The cache holds keys and values in pages of page_size tokens. Token j of
+ * sequence b lives in page block_table[b][j / page_size] at place
+ * j % page_size; its key of head h starts at element
+ *   page * page_stride + (j % page_size) * token_stride + h * head_stride
+ * of `k` (its value at the same element of `v`), head_dim values contiguous.
+ * Any order of page, token and head fits (heads outermost within a page gives
+ * the longest contiguous runs: head_stride = page_size * head_dim).
+ *   dtype        QGEMM_DT_F16, QGEMM_DT_BF16 (must be the call's act_dtype) or
+ *                QGEMM_DT_FP8: e4m3 codes; a key is its code times k_scale, a
+ *                value its code times v_scale (finite, > 0). The scales must be 1
+ *                for the 16-bit types.
+ *   page_size    a multiple of 16, 16..65536; num_pages 1..2^31-1
+ *   kv_heads     1..1024; head_dim a multiple of 16, 16..256
+ *   strides      multiples of 16 bytes; token_stride head_dim..2^25 elements,
+ *                head_stride >= head_dim where kv_heads > 1; 0 <= page_stride
+ *   k, v         16-byte aligned, caller-owned like every buffer
+ * block_table is int32 [num_seqs][table_stride], device memory. An entry outside
+ * 0..num_pages-1 is never followed: its tokens count as masked (attention) or
+ * are not stored (append), so entries past a sequence's end may hold anything.
+ *
+ * Strides of q, k, v, q_out and out are in elements: head h of token t starts at
+ * t * token_stride + h * head_stride, with head_dim values contiguous, 16-byte
+ * aligned; so the parts of one fused product's output serve without a copy.
+ * act_dtype is QGEMM_DT_F16 or QGEMM_DT_BF16. q_heads is a multiple of kv_heads
+ * of at most 128 times it: query head h reads key-value head
+ * h / (q_heads / kv_heads). num_seqs and num_tokens are at most 65535 and 2^20
+ * (0: nothing is launched), max_len at most 2^24 and at most
+ * table_stride * page_size.
+ */
+typedef struct qgemm_kv_cache {
+  void* k;
+  void* v;
+  int64_t num_pages;
+  int64_t page_stride, token_stride, head_stride; /* elements */
+  int32_t page_size;                              /* tokens */
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;                                  /* qgemm_dtype */
+  float k_scale, v_scale;
+} qgemm_kv_cache;
+
+/*
+ * Norms of queries and keys per head, position rotation, and the store of keys
+ * and values into the cache, in one pass over num_tokens new tokens.
+ *   norm      y = x / sqrt(mean(x^2) + eps) * w, per head, with w = q_norm or
+ *             k_norm (act_dtype [head_dim]; NULL: that operand is not normed)
+ *   rotation  the first rot_dim values of a head (a multiple of 16, 0..head_dim)
+ *             in pairs (a, b) -> (a cos - b sin, b cos + a sin): pair i is
+ *             (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved != 0; cos and
+ *             sin are entries i and rot_dim/2 + i of row `position` of `rope`,
+ *             fp32 [rope_rows][rot_dim] (may be NULL when rot_dim is 0)
+ *   store     q to q_out (act_dtype); k and v to the cache at `position` of
+ *             sequence token_seq[t] (int32 [num_tokens]; NULL: token t belongs
+ *             to sequence t), e4m3 caches as round(x / scale), saturated at +-448
+ * All arithmetic is fp32 with one rounding per stored value. positions is int32
+ * [num_tokens]; a token whose position is negative or at least rope_rows is
+ * padding: its q_out rows are zero and nothing is stored. A token whose
+ * sequence, table entry or page is out of range is rotated but not stored. Two
+ * tokens for the same place race. q_out may be q itself (same strides);
+ * otherwise it must not overlap an input. rope_rows bounds positions also when
+ * rot_dim is 0.
+ */
+int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                         int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_token_stride, int64_t v_head_stride, const void* q_norm,
+                         const void* k_norm, float eps, const float* rope, int64_t rope_rows,
+                         int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                         const int32_t* token_seq, const int32_t* block_table, int64_t table_stride,
+                         int64_t num_seqs, int64_t num_tokens, int32_t q_heads, int32_t act_dtype,
+                         const qgemm_kv_cache* cache, void* q_out, int64_t qo_token_stride,
+                         int64_t qo_head_stride, void* stream);
+
+/*
+ * Attention of one new token per sequence over its cached tokens
+ * (j < n, n = seq_lens[b], the new token's own included):
+ *   out[b,h] = sum_j softmax_j(scale * q[b,h] . k[j]) v[j]
+ * window = 0: every j < n is visible; window > 0: the last `window` tokens and
+ * the first `sinks` ones (j >= n - window or j < sinks) are. Masked keys and
+ * values are never used, whatever their memory holds. A sequence without visible
+ * tokens (n <= 0, or no page in range) gives zeros. seq_lens is int32
+ * [num_seqs] in device memory; lengths above max_len are taken as max_len.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
+ * to 16 bits for the matrix cores (fp16, or act_dtype's bfloat16 against a
+ * bfloat16 cache), each output once to act_dtype. scale must be finite and > 0.
+ *
+ * The cache's length is split over workgroups when there are few rows; the last
+ * workgroup of a row joins the parts in order, so results do not change from run
+ * to run. The workspace contract is qgemm_workspace_bytes' (zeroed once; counters
+ * are left zero); one workspace serves GEMM and attention calls alike.
+ */
+int qgemm_attn_decode_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t q_heads,
+                                      int32_t kv_heads, int32_t head_dim, int64_t window,
+                                      int32_t sinks, size_t* bytes);
+int qgemm_attn_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                      const qgemm_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                      const int32_t* seq_lens, int64_t num_seqs, int64_t max_len, int32_t q_heads,
+                      int32_t act_dtype, float scale, int64_t window, int32_t sinks, void* out,
+                      int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention of several new tokens per sequence: rows q_start[b] ..
+ * q_start[b+1]-1 of q and out (int32 [num_seqs + 1] in device memory,
+ * nondecreasing) are the last tokens of sequence b, whose cache holds
+ * n = seq_lens[b] tokens with them. Row i of its m rows stands at position
+ * p = n - m + i and sees j <= p with (window = 0, or j > p - window, or
+ * j < sinks). Rows at a negative position give zeros. No sequence may have more
+ * than max_q rows (the rows past max_q are left unwritten, as are rows of q that
+ * belong to no sequence); row numbers are bounded by num_tokens. A key or value
+ * that some row of a sequence sees has to be finite: rows share the matrix
+ * products of a tile, so an infinite or NaN value there may reach rows that do
+ * not see it. Everything else as for qgemm_attn_decode.
+ */
+int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t max_len,
+                                       int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int64_t window, int32_t sinks, size_t* bytes);
+int qgemm_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                       const qgemm_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                       const int32_t* q_start, const int32_t* seq_lens, int64_t num_seqs,
+                       int64_t num_tokens, int64_t max_q, int64_t max_len, int32_t q_heads,
+                       int32_t act_dtype, float scale, int64_t window, int32_t sinks, void* out,
+                       int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Force the number of parts into which later attention calls of this process
+ * split the cache's length (1..1024; 0: automatic). For tests and tuning, like
+ * qgemm_set_plan_override; affects the attention workspace queries too.
+ */
+int qgemm_attn_set_splits(int splits);
 
 /*
  * Work decomposition used for a call of this shape (for tests and tuning).
