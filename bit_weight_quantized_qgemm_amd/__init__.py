@@ -202,6 +202,12 @@ def _stream_ptr(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream's handle of a device, without building a Stream object
+    (0.1 us against 2 us, of calls that take about 10)."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
@@ -229,12 +235,14 @@ class Workspace:
         self._bufs = {}
 
     def get(self, nbytes: int, device):
-        torch = _torch()
-        idx = torch.device(device).index if torch.device(device).index is not None else torch.cuda.current_device()
-        key = (idx, torch.cuda.current_stream(idx).cuda_stream)
-        buf = self._bufs.get(key)
         if nbytes == 0:
             return None, 0
+        torch = _torch()
+        idx = torch.device(device).index
+        if idx is None:
+            idx = torch.cuda.current_device()
+        key = (idx, _raw_stream(idx))
+        buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
             buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
             self._bufs[key] = buf

@@ -12,7 +12,7 @@ import ctypes
 import functools
 import math
 
-from . import (DT_BF16, DT_F16, DT_FP8, Workspace, _check, _default_ws, _ptr, _stream_ptr, _torch, lib)
+from . import DT_BF16, DT_F16, DT_FP8, Workspace, _check, _default_ws, _raw_stream, _torch, lib
 
 __all__ = ["KVCache", "rope_table", "qk_rope_append", "attn_decode", "attn_prefill", "set_attn_splits",
            "attn_decode_workspace_bytes", "attn_prefill_workspace_bytes"]
@@ -46,6 +46,7 @@ class KVCache:
         if k.stride(3) != 1:
             raise ValueError("a head's values must be contiguous")
         self.k, self.v, self.device = k, v, k.device
+        self._index = k.device.index   # of the device whose current stream the calls use
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.num_pages, k.stride(0), k.stride(1), k.stride(2),
@@ -74,30 +75,46 @@ def rope_table(rows: int, rot_dim: int, theta: float = 10000.0, device=None):
     return torch.cat([angle.cos(), angle.sin()], dim=1).to(torch.float32).to(device)
 
 
-def _int32(t, name: str, device, *shape):
+def _int32(t, name: str, device, shape):
     if t.dtype != _torch().int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
-    if len(shape) != t.dim() or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _heads(t, name: str, heads, cache: KVCache, dtype=None):
-    """Checks a [tokens][heads][head_dim] tensor (any token and head stride)."""
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens][heads][head_dim], got {tuple(t.shape)}")
-    if t.stride(2) != 1:
-        raise ValueError(f"{name}: a head's values must be contiguous")
+def _table(t, device):
+    if t.dim() != 2:
+        raise ValueError("block_table must be [sequences][columns]")
+    _int32(t, "block_table", device, t.shape)
+
+
+def _heads(t, name: str, shape, cache: KVCache, dtype):
+    """Checks a [tokens][heads][head_dim] tensor (any token and head stride); returns (pointer, strides)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] = {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != cache.device:
         raise ValueError(f"{name} must live on the cache's device")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    ts, hs, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: a head's values must be contiguous")
+    return t.data_ptr(), ts, hs
 
 
-def _act(t) -> int:
-    dt = _dtypes().get(t.dtype)
+def _queries(q, cache: KVCache, out):
+    """Checks q and out (a new tensor if None): (shape, type id, out, q's pointer and strides, out's)."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [tokens][heads][head_dim of the cache], not {tuple(shape)}")
+    dt = _dtypes().get(q.dtype)
     if dt is None or dt == DT_FP8:
         raise ValueError("activations must be float16 or bfloat16")
-    return dt
+    qa = _heads(q, "q", shape, cache, q.dtype)
+    if out is None:
+        torch = _torch()
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    return shape, dt, out, qa, _heads(out, "out", shape, cache, q.dtype)
 
 
 def qk_rope_append(q, k, v, positions, cache: KVCache, block_table, rope=None, q_norm=None, k_norm=None,
@@ -109,36 +126,29 @@ def qk_rope_append(q, k, v, positions, cache: KVCache, block_table, rope=None, q
     one fused product's output as they are); positions int32 [tokens] (negative: padding); block_table int32
     [sequences][columns]; token_seq int32 [tokens], or None when token t is sequence t's. `out` may be q."""
     torch = _torch()
-    T, H, dev = q.shape[0], q.shape[1], cache.device
-    _heads(q, "q", None, cache)
-    _heads(k, "k", cache.kv_heads, cache, q.dtype)
-    _heads(v, "v", cache.kv_heads, cache, q.dtype)
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v must have one row per token")
-    _int32(positions, "positions", dev, T)
-    _int32(block_table, "block_table", dev, None, None)
+    dev = cache.device
+    shape, dt, out, qa, oa = _queries(q, cache, out)
+    T, H, D = shape
+    kv_shape = (T, cache.kv_heads, D)
+    ka, va = _heads(k, "k", kv_shape, cache, q.dtype), _heads(v, "v", kv_shape, cache, q.dtype)
+    _int32(positions, "positions", dev, (T,))
+    _table(block_table, dev)
     if token_seq is not None:
-        _int32(token_seq, "token_seq", dev, T)
+        _int32(token_seq, "token_seq", dev, (T,))
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and (w.dtype != q.dtype or w.device != dev or tuple(w.shape) != (cache.head_dim,)
-                              or not w.is_contiguous()):
+        if w is not None and (w.dtype != q.dtype or w.device != dev or w.shape != (D,) or not w.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous [head_dim] tensor of q's type")
     rows, rot = 1 << 24, 0
     if rope is not None:
         if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != dev or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 [positions][rot_dim] tensor")
         rows, rot = rope.shape
-    if out is None:
-        out = torch.empty((T, H, cache.head_dim), dtype=q.dtype, device=dev)
-    else:
-        _heads(out, "out", H, cache, q.dtype)
-        if out.shape[0] != T:
-            raise ValueError("out must have one row per token")
+    seqs, cols = block_table.shape
     _check(lib().qgemm_qk_rope_append(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-        v.stride(1), _ptr(q_norm), _ptr(k_norm), eps, _ptr(rope), rows, rot, int(interleaved), positions.data_ptr(),
-        _ptr(token_seq), block_table.data_ptr(), block_table.shape[1], block_table.shape[0], T, H, _act(q), cache._ref,
-        out.data_ptr(), out.stride(0), out.stride(1), _stream_ptr(dev)), "qgemm_qk_rope_append")
+        *qa, *ka, *va, None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+        eps, None if rope is None else rope.data_ptr(), rows, rot, 1 if interleaved else 0, positions.data_ptr(),
+        None if token_seq is None else token_seq.data_ptr(), block_table.data_ptr(), cols, seqs, T, H, dt, cache._ref,
+        *oa, _raw_stream(cache._index)), "qgemm_qk_rope_append")
     return out
 
 
@@ -163,18 +173,11 @@ def attn_prefill_workspace_bytes(num_seqs: int, max_q: int, max_len: int, q_head
     return out.value
 
 
-def _attn_args(q, cache, block_table, seq_lens, out):
-    torch = _torch()
-    dev = cache.device
-    _heads(q, "q", None, cache)
-    _int32(block_table, "block_table", dev, None, None)
-    _int32(seq_lens, "seq_lens", dev, block_table.shape[0])
-    if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _heads(out, "out", q.shape[1], cache, q.dtype)
-    if out.shape[0] != q.shape[0]:
-        raise ValueError("out must have q's shape")
-    return out
+def _workspace(workspace, cache, nbytes):
+    if nbytes == 0:
+        return None, 0
+    ws, wsb = (workspace or _default_ws).get(nbytes, cache.device)
+    return ws.data_ptr(), wsb
 
 
 def attn_decode(q, cache: KVCache, block_table, seq_lens, max_len: int, scale: float | None = None, window: int = 0,
@@ -183,16 +186,20 @@ def attn_decode(q, cache: KVCache, block_table, seq_lens, max_len: int, scale: f
     [head_dim], block_table int32 [sequences][columns], seq_lens int32 [sequences], all at most max_len (a host number,
     so that the call reads nothing back). window > 0 shows the last `window` tokens and the first `sinks`. scale
     defaults to head_dim ** -0.5. Returns q's shape and type."""
-    out = _attn_args(q, cache, block_table, seq_lens, out)
-    B, H, D = q.shape
-    if B != block_table.shape[0]:
+    shape, dt, out, qa, oa = _queries(q, cache, out)
+    B, H, D = shape
+    dev = cache.device
+    _table(block_table, dev)
+    seqs, cols = block_table.shape
+    if B != seqs:
         raise ValueError("q must have one row per sequence")
-    ws, wsb = (workspace or _default_ws).get(
-        attn_decode_workspace_bytes(B, max_len, H, cache.kv_heads, D, window, sinks), cache.device)
+    _int32(seq_lens, "seq_lens", dev, (B,))
+    ws, wsb = _workspace(workspace, cache,
+                         attn_decode_workspace_bytes(B, max_len, H, cache.kv_heads, D, window, sinks))
     _check(lib().qgemm_attn_decode(
-        q.data_ptr(), q.stride(0), q.stride(1), cache._ref, block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), B, max_len, H, _act(q), 1.0 / math.sqrt(D) if scale is None else scale, window, sinks,
-        out.data_ptr(), out.stride(0), out.stride(1), _ptr(ws), wsb, _stream_ptr(cache.device)), "qgemm_attn_decode")
+        *qa, cache._ref, block_table.data_ptr(), cols, seq_lens.data_ptr(), B, max_len, H, dt,
+        1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb, _raw_stream(cache._index)),
+        "qgemm_attn_decode")
     return out
 
 
@@ -203,15 +210,17 @@ def attn_prefill(q, cache: KVCache, block_table, q_start, seq_lens, max_q: int, 
     [head_dim] are the last tokens of sequence b, whose cache holds seq_lens[b] tokens with them. q_start int32
     [sequences + 1]; max_q and max_len bound the rows and lengths of every sequence (host numbers). Otherwise as
     attn_decode."""
-    out = _attn_args(q, cache, block_table, seq_lens, out)
-    T, H, D = q.shape
-    B = block_table.shape[0]
-    _int32(q_start, "q_start", cache.device, B + 1)
-    ws, wsb = (workspace or _default_ws).get(
-        attn_prefill_workspace_bytes(B, max_q, max_len, H, cache.kv_heads, D, window, sinks), cache.device)
+    shape, dt, out, qa, oa = _queries(q, cache, out)
+    T, H, D = shape
+    dev = cache.device
+    _table(block_table, dev)
+    seqs, cols = block_table.shape
+    _int32(q_start, "q_start", dev, (seqs + 1,))
+    _int32(seq_lens, "seq_lens", dev, (seqs,))
+    ws, wsb = _workspace(workspace, cache,
+                         attn_prefill_workspace_bytes(seqs, max_q, max_len, H, cache.kv_heads, D, window, sinks))
     _check(lib().qgemm_attn_prefill(
-        q.data_ptr(), q.stride(0), q.stride(1), cache._ref, block_table.data_ptr(), block_table.shape[1],
-        q_start.data_ptr(), seq_lens.data_ptr(), B, T, max_q, max_len, H, _act(q),
-        1.0 / math.sqrt(D) if scale is None else scale, window, sinks, out.data_ptr(), out.stride(0), out.stride(1),
-        _ptr(ws), wsb, _stream_ptr(cache.device)), "qgemm_attn_prefill")
+        *qa, cache._ref, block_table.data_ptr(), cols, q_start.data_ptr(), seq_lens.data_ptr(), seqs, T, max_q, max_len,
+        H, dt, 1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb,
+        _raw_stream(cache._index)), "qgemm_attn_prefill")
     return out

@@ -143,8 +143,22 @@ qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
   const int64_t blocks = visible_blocks(max_len, 1, window, sinks);
   constexpr int kStep = 2 * qg::kDecodeWaves;   // one pair of blocks for each wave
-  const int64_t fill = 4 * (int64_t)qg::device_cu_count();
-  split(pl, blocks, std::min(fill / pl.tiles, (blocks + kStep - 1) / kStep), kStep, head_dim);
+  // Few tiles: one part per compute unit, which streams as fast as more parts and
+  // joins fewer (measured, 64/8 heads of 128, us: 1 x 131072 tokens, e4m3, 47 with
+  // 256 workgroups, 51 with 512; 4 x 16384 of one length 46, 51 with 1024). More
+  // tiles, up to two per unit: four parts per unit, because the parts of
+  // sequences of different lengths are evened out by the order in which they
+  // start (16 ragged contexts up to 8192: 59 with 1024 workgroups, 68 with 256;
+  // of one length 88 and 84). Beyond, the tiles themselves do that (64 ragged
+  // contexts up to 2048: 62 unsplit and in two parts; of one length 82 and 90).
+  // Heads above 128 values leave room for one workgroup per unit: one part each
+  // (16 contexts of 4000, 32/8 heads of 256: 85 with 256 workgroups, 101 with 1024).
+  const int64_t cus = qg::device_cu_count();
+  const int64_t fill = pl.tiles >= 2 * cus ? 0 : pl.tiles > cus / 4 && head_dim <= 128 ? 4 * cus : cus;
+  // The join reads 16 parts at a time: more of them only while each keeps four
+  // steps (4 x 8192, 16/1 heads: 15 in 16 parts, 21 in 64 of one step each).
+  const int64_t steps = (blocks + kStep - 1) / kStep;
+  split(pl, blocks, std::min({fill / pl.tiles, steps, std::max<int64_t>(16, steps / 4)}), kStep, head_dim);
   return pl;
 }
 
@@ -156,9 +170,27 @@ qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int 
   pl.part_rows = (int)std::min<int64_t>(rows, qg::kPrefillRows);
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
   const int64_t blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), window, sinks);
-  constexpr int kStep = 4;   // blocks of a tile of K and V
-  const int64_t fill = 2 * (int64_t)qg::device_cu_count();
-  split(pl, blocks, std::min(fill / pl.tiles, (blocks + kStep - 1) / kStep), kStep, head_dim);
+  // Tiles of K and V hold 64 tokens (32 for heads above 128 values). One takes a
+  // workgroup that has a compute unit for itself about 1.25 us, one of two that
+  // share a unit 2.3 us, and joining s parts 6 + s / 4 us (measured; e.g. 2 x 5 new
+  // tokens on 6001, 64/8 heads of 128, 16 row tiles: 120 us unsplit, 20 in 16 parts,
+  // 23 in 32; 64 on 16384, 32 row tiles: 326, 56 in 8 parts, 52 in 16; 512 on
+  // nothing, 256 row tiles: 19, 31 in 2 parts).
+  const int kStep = head_dim <= 128 ? 4 : 2;   // blocks of a tile of K and V
+  const int64_t steps = (blocks + kStep - 1) / kStep, cus = qg::device_cu_count();
+  const int64_t resident = head_dim <= 128 ? 2 : 1;   // workgroups of a compute unit
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t s : {int64_t(1), cus / pl.tiles, resident * cus / pl.tiles}) {
+    s = std::max<int64_t>(1, std::min(s, steps));
+    const double alone = pl.tiles * s <= cus ? 1.25 : 2.3 * std::max(1.0, (double)(pl.tiles * s) / (2 * cus));
+    const double cost = (double)((steps + s - 1) / s) * alone + (s > 1 ? 6 + 0.25 * s : 0);
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  split(pl, blocks, best, kStep, head_dim);
   return pl;
 }
 

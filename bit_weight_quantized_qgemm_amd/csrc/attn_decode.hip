@@ -48,7 +48,7 @@ struct PairAt {
 };
 
 template <class F, class PF, bool FP8, int DP, bool EXACT>
-__global__ void __launch_bounds__(256) attn_decode(AttnArgs p) {
+__global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_decode(AttnArgs p) {
   using S = DecodeShape<F, FP8, DP>;
   using T = typename F::T;
   constexpr int kOutStride = DP + 4;
@@ -58,10 +58,15 @@ __global__ void __launch_bounds__(256) attn_decode(AttnArgs p) {
 
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-  const int row_tile = tile % p.row_tiles;
-  const int kv_head = tile / p.row_tiles % p.kv_heads;
-  const int seq = tile / p.row_tiles / p.kv_heads;
+  // all first parts, then all second ones: the parts that a shorter sequence does
+  // not have come last, and workgroups 8 apart, which share an XCD, hold every
+  // part number in equal shares
+  const int heads = p.kv_heads * p.row_tiles;
+  const int tiles = p.num_seqs * heads;
+  const int split = p.splits == 1 ? 0 : (int)(blockIdx.x / (uint32_t)tiles), tile = blockIdx.x - split * tiles;
+  const int seq = (int)((uint32_t)tile / (uint32_t)heads);
+  const int row_tile = p.row_tiles == 1 ? 0 : (tile - seq * heads) % p.row_tiles;
+  const int kv_head = p.row_tiles == 1 ? tile - seq * heads : (tile - seq * heads) / p.row_tiles;
   const int head0 = kv_head * p.group + row_tile * kDecodeRows;
   const int rows = min(kDecodeRows, p.group - row_tile * kDecodeRows);
 
@@ -306,14 +311,16 @@ __global__ void __launch_bounds__(256) attn_decode(AttnArgs p) {
     part_max[wave][lane] = mref;
     part_sum[wave][lane] = sum;
   }
+  if (c < rows) {
 #pragma unroll
-  for (int j = 0; j < S::kVCols; ++j)
+    for (int j = 0; j < S::kVCols; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int i = 0; i < S::kVDims; i += 4)
-        *reinterpret_cast<f32x4*>(&part[wave][c][j * 16 * S::kVDims + (4 * h + r) * S::kVDims + i]) =
-            f32x4{acc[j][i][r], acc[j][i + 1][r], acc[j][i + 2][r], acc[j][i + 3][r]};
+        for (int i = 0; i < S::kVDims; i += 4)
+          *reinterpret_cast<f32x4*>(&part[wave][c][j * 16 * S::kVDims + (4 * h + r) * S::kVDims + i]) =
+              f32x4{acc[j][i][r], acc[j][i + 1][r], acc[j][i + 2][r], acc[j][i + 3][r]};
+  }
   __syncthreads();
 
   const int quads = p.head_dim / 4;   // fp32 quadruples of a row
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(256) attn_decode(AttnArgs p) {
   float* stats = p.stats + part_id * p.part_rows * 2;
   const rsrc_t out_r = make_rsrc(p.partial + part_id * p.part_rows * p.head_dim, (uint32_t)(p.part_rows * p.head_dim * 4));
   for (int x = threadIdx.x; x < rows * quads; x += 256) {
-    const int row = x / quads, d = 4 * (x - row * quads);
+    const int row = EXACT ? x / (DP / 4) : x / quads, d = 4 * (x - row * quads);
     float m = part_max[0][row];
 #pragma unroll
     for (int w = 1; w < kDecodeWaves; ++w) m = fmaxf(m, part_max[w][row]);

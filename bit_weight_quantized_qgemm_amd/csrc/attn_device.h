@@ -28,6 +28,10 @@ struct F16 {
   static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   }
+  // sum of a pair's values, and acc
+  static __device__ __forceinline__ float add_pair(uint32_t w, float acc) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{1, 1}, acc, false);
+  }
   // two e4m3 codes (the low or high half of a word) as a pair; exact
   template <bool HIGH>
   static __device__ __forceinline__ uint32_t from_fp8(uint32_t w) {
@@ -47,6 +51,9 @@ struct BF16 {
   }
   static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float add_pair(uint32_t w, float acc) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), bf16x2{1, 1}, acc, false);
   }
   template <bool HIGH>
   static __device__ __forceinline__ uint32_t from_fp8(uint32_t w) {
@@ -92,7 +99,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& p, int tile, int part
   const int64_t part_elems = (int64_t)p.part_rows * p.head_dim;
   const float* stats = p.stats + (int64_t)tile * p.splits * p.part_rows * 2;
   const float* partial = p.partial + (int64_t)tile * p.splits * part_elems;
-  constexpr int kBatch = 8;   // parts whose loads are in flight together
+  constexpr int kBatch = 16;   // parts whose loads are in flight together
   for (int x = threadIdx.x; x < rows * quads; x += blockDim.x) {
     const int row = x / quads, d = 4 * (x - row * quads);
     float m = kNegInf, total = 0.f;

@@ -3,13 +3,13 @@
 // A workgroup of four waves takes 128 rows of one sequence and key-value head. A
 // row is one query head of one new token, the heads of a token side by side, so
 // heads that share keys share the workgroup's tiles of K and V. Each wave owns 32
-// rows as the columns of 32x32x16 matrix products: scores S^T = K q^T of 64
+// rows as the columns of 32x32x16 matrix products: scores S^T = K q^T of 32
 // tokens at a time, a running maximum and sum per row in registers (fp32), and
 // outputs O^T = V^T P^T.
 //
-// Tiles of K and V (64 tokens, four 16-token blocks of any four pages) go through
-// registers into two LDS buffers in turn, one barrier per tile: wave w loads block
-// w of the next tile while the current one is used.
+// Tiles of K and V (64 tokens of any four 16-token blocks; 32 for heads above 128
+// values) go to LDS, three slots of K and two of V, with one barrier per tile: in
+// the turn of tile t, V of tile t + 1 and K of tile t + 2 are on their way.
 //   K    rows of 16-byte chunks, chunk number xor token, so that the 16 tokens that
 //        are read together (one chunk each) lie in different banks.
 //   V    rows as in memory; the operand wants 4 consecutive tokens of one dimension
@@ -19,8 +19,10 @@
 //   P    the scores leave the matrix unit with row c and tokens 8x + 4h .. + 3 in
 //        lane (c, h) = (lane % 32, lane / 32): two such runs are the second operand
 //        of the next product as they stand, if V's tokens come in the same order.
-// The weights P are rounded once to 16 bits for the matrix unit; statistics,
-// sums and accumulators stay fp32.
+// The scores of the next 32 tokens are computed beside the exponentials of the
+// present ones, so the matrix and vector units of a SIMD work at the same time in
+// each of its two waves. The weights P are rounded once to 16 bits for the matrix
+// unit, and summed as rounded; statistics, sums and accumulators stay fp32.
 #include "attn_device.h"
 
 namespace qg {
@@ -28,141 +30,258 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
+typedef const __attribute__((address_space(3))) u32x4* lds_u32x4_t;
+typedef const __attribute__((address_space(3))) char* lds_char_t;
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kTile = 64;                       // tokens of a tile
-constexpr int kTileBlocks = kTile / kTokBlock;  // one per wave
+// A raw buffer resource as its four words, for the loads below.
+__device__ __forceinline__ u32x4 rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, (uint32_t)kRsrcWord3};
+}
+// 16 bytes per lane straight into LDS, in lane order from byte `dst` on; lanes past
+// the resource write zeros. Written out because the compiler waits for every such
+// load that it knows of before any LDS read that it cannot tell apart from it (it
+// cannot, for the transposing ones), which would undo the prefetch. It has no
+// register result; its arrival is waited for by hand (wait_loads).
+__device__ __forceinline__ void dma_16(u32x4 r, uint32_t dst, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(dst), "v"(voff), "s"(r), "s"(soff)
+               : "memory", "m0");
+}
+// At most N vector-memory operations of this wave are still in flight; nothing
+// moves across.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Barrier of the workgroup without a wait for loads in flight; this wave's LDS
+// writes are complete.
+__device__ __forceinline__ void lds_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0) alone
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+constexpr int kPrefillWaves = 4;
 
 template <int DP>
 struct PrefillLds {
-  static constexpr int kRow = DP * 2;             // bytes of a token
-  static constexpr int kBytes = kTile * kRow;     // K or V of a tile
-  static constexpr int kTotal = 4 * kBytes;       // two buffers
+  static constexpr int kTile = DP <= 128 ? 64 : 32;   // tokens of a tile
+  static constexpr int kRow = DP * 2;                  // bytes of a token
+  static constexpr int kBytes = kTile * kRow;          // a slot
+  static constexpr int kV = 3 * kBytes;                // the first slot of V
+  static constexpr int kTotal = 5 * kBytes;
   // byte place of 16-byte chunk c of token t
-  static __device__ __forceinline__ int k_at(int t, int c) {
-    const int x = DP == 64 ? (t >> 1) & 7 : t & 15;
-    return t * kRow + ((c ^ x) << 4);
-  }
-  static __device__ __forceinline__ int v_at(int t, int c) {
-    const int x = DP == 64 ? (t >> 1) & 1 : t & 3;
-    return t * kRow + ((c ^ (x << 2)) << 4);
-  }
+  static __device__ __forceinline__ int k_turn(int t) { return DP == 64 ? (t >> 1) & 7 : t & 15; }
+  static __device__ __forceinline__ int v_turn(int t) { return (DP == 64 ? (t >> 1) & 1 : t & 3) << 2; }
+  static __device__ __forceinline__ int k_at(int t, int c) { return t * kRow + ((c ^ k_turn(t)) << 4); }
+  static __device__ __forceinline__ int v_at(int t, int c) { return t * kRow + ((c ^ v_turn(t)) << 4); }
 };
 
-template <class F, class PF, bool FP8, int DP, bool EXACT>
-__device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds, int* flag) {
-  using L = PrefillLds<DP>;
-  using T = typename F::T;
-  constexpr int kElt = FP8 ? 1 : 2;
-  constexpr int kLanes = DP * kElt / 16;          // lanes that load one token
-  constexpr int kRows = 64 / kLanes;              // tokens of a load
-  constexpr int kLoads = kTokBlock / kRows;       // loads of a block
-  constexpr int kSteps = DP / 16;
-  constexpr int kDB = DP / 32;
-
-  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // key-value heads innermost: the workgroups of one head, which read the same
-  // tiles, land on one XCD where there are 8 of them (or a multiple); the last
-  // rows, which see most, first; parts of one row tile apart
-  const int tiles = p.num_seqs * p.kv_heads * p.row_tiles;
-  const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
-  const int kv_head = tile % p.kv_heads;
-  const int seq = tile / p.kv_heads % p.num_seqs;
-  const int row0 = (p.row_tiles - 1 - tile / p.kv_heads / p.num_seqs) * kPrefillRows;
-
+// A row tile: its sequence, rows and what they see.
+struct RowTile {
+  int seq, kv_head, row0, rows, all_rows;
+  int q0;                   // first row of q of the sequence
+  int pos0;                 // position of the first new token
+  int pos_min, pos_max;
+  Visible see;              // what any of its rows sees
+  int parts;
+};
+// Key-value heads innermost: the workgroups of one head, which read the same
+// tiles, land on one XCD where there are 8 of them (or a multiple); the last rows,
+// which see most, first.
+__device__ __forceinline__ RowTile row_tile_of(const AttnArgs& p, int tile) {
+  const uint32_t t = (uint32_t)tile / (uint32_t)p.kv_heads;
+  const int kv_head = tile - (int)t * p.kv_heads;
+  const int back = (int)(t / (uint32_t)p.num_seqs), seq = (int)t - back * p.num_seqs;
+  const int row0 = (p.row_tiles - 1 - back) * kPrefillRows;
   const int len = min(max(scalar_load(p.lens + seq), 0), p.max_len);
   const int q0 = min(max(scalar_load(p.q_start + seq), 0), p.num_tokens);
   const int q1 = min(max(scalar_load(p.q_start + seq + 1), q0), p.num_tokens);
   const int new_tokens = min(q1 - q0, p.max_q);
   const int all_rows = new_tokens * p.group;
-  if (row0 >= all_rows) return;
-  const int rows = min(kPrefillRows, all_rows - row0);
-  const int pos0 = len - new_tokens;              // position of the first new token
-  const int pos_min = pos0 + row0 / p.group, pos_max = pos0 + (row0 + rows - 1) / p.group;
+  const int rows = min(kPrefillRows, all_rows - row0);   // <= 0: none
+  const int pos0 = len - new_tokens;
+  const int pos_min = pos0 + (int)((uint32_t)row0 / (uint32_t)p.group);
+  const int pos_max = pos0 + (int)((uint32_t)(row0 + max(1, rows) - 1) / (uint32_t)p.group);
   const Visible see(max(0, pos_max + 1), p.window ? pos_min - p.window + 1 : 0, p.window ? p.sinks : 0);
-  const int parts = max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks);
-  if (split >= parts) return;
+  const int parts = p.splits == 1 ? 1 : max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks);
+  return RowTile{seq, kv_head, row0, rows, all_rows, q0, pos0, pos_min, pos_max, see, parts};
+}
+
+template <class F, class PF, bool FP8, int DP, bool EXACT>
+__device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
+  using L = PrefillLds<DP>;
+  using T = typename F::T;
+  constexpr int kElt = FP8 ? 1 : 2;
+  constexpr int kBlocks = L::kTile / kTokBlock;       // blocks of a tile
+  constexpr int kHalves = L::kTile / 32;              // steps of a tile
+  constexpr int kMine = L::kTile / kPrefillWaves;     // tokens of a tile that a wave loads
+  constexpr int kLanes = DP * kElt / 16;              // lanes that load one token
+  constexpr int kRows = 64 / kLanes;                  // tokens of a load
+  constexpr int kLoads = kMine / kRows;
+  constexpr int kSteps = DP / 16;
+  constexpr int kDB = DP / 32;
+
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = p.num_seqs * p.kv_heads * p.row_tiles;
+  const int split = p.splits == 1 ? 0 : (int)(blockIdx.x / (uint32_t)tiles), tile = blockIdx.x - split * tiles;
+  const RowTile rt = row_tile_of(p, tile);
+  if (rt.rows <= 0 || split >= rt.parts) return;
+  const Visible& see = rt.see;
   const int v_begin = split * p.split_blocks, v_end = min(see.blocks, v_begin + p.split_blocks);
+  const int turns = (v_end - v_begin + kBlocks - 1) / kBlocks;   // tiles
 
   // ---- this lane's row, and the wave's span of positions
-  const int row = row0 + wave * 32 + c;
-  const bool live = row < all_rows;
-  const int qi = live ? row / p.group : 0;
-  const int head = kv_head * p.group + (live ? row - qi * p.group : 0);
-  const int pos = live ? pos0 + qi : -1;
+  const int row = rt.row0 + wave * 32 + c;
+  const bool live = row < rt.all_rows;
+  const int qi = live ? (int)((uint32_t)row / (uint32_t)p.group) : 0;
+  const int head = rt.kv_head * p.group + (live ? row - qi * p.group : 0);
+  const int pos = live ? rt.pos0 + qi : -1;
   const int low = p.window ? pos - p.window + 1 : 0;
-  const int wave_rows = min(32, rows - wave * 32);   // may be <= 0
-  const int wave_min = pos0 + (row0 + wave * 32) / p.group;
-  const int wave_max = wave_rows > 0 ? pos0 + (row0 + wave * 32 + wave_rows - 1) / p.group : -1;
+  const int wave_rows = min(32, rt.rows - wave * 32);   // may be <= 0
+  const int wave_min = rt.pos0 + (int)((uint32_t)(rt.row0 + wave * 32) / (uint32_t)p.group);
+  const int wave_max =
+      wave_rows > 0 ? rt.pos0 + (int)((uint32_t)(rt.row0 + wave * 32 + wave_rows - 1) / (uint32_t)p.group) : -1;
   const int wave_low = p.window ? wave_max - p.window + 1 : 0;   // every row of the wave sees low..min
 
   u32x4 q[kSteps];
-  {
-    const T* src = static_cast<const T*>(p.q) + (int64_t)(q0 + qi) * p.q_ts + head * p.q_hs;
+  auto load_q = [&]() {
+    const T* src = static_cast<const T*>(p.q) + (int64_t)(rt.q0 + qi) * p.q_ts + head * p.q_hs;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int d = 16 * s + 8 * h;
       q[s] = u32x4{0, 0, 0, 0};
       if (live && d < p.head_dim) q[s] = *reinterpret_cast<const u32x4*>(src + d);
     }
-  }
+  };
 
-  // ---- loads: this wave's block of a tile
-  const int32_t* table = p.cache.table + seq * p.cache.table_stride;
-  const uint32_t ts_bytes = (uint32_t)p.cache.token_stride * kElt;
-  const char* kbase = static_cast<const char*>(p.cache.k) + kv_head * p.cache.head_stride * kElt;
-  const char* vbase = static_cast<const char*>(p.cache.v) + kv_head * p.cache.head_stride * kElt;
-  const int l_row = lane / kLanes, l_chunk = lane % kLanes;
-  const uint32_t voff = EXACT || l_chunk * 16 < p.head_dim * kElt ? l_row * ts_bytes + l_chunk * 16 : 0x80000000u;
-  u32x4 kr[kLoads], vr[kLoads];
-  int ld_blk = 0;
-  // page of virtual block v, or -1
-  auto page_at = [&](int v, int* blk, int* place) {
-    const bool there = v < v_end;
-    *blk = there ? see.block(v) : 0;
-    const int col = page_of(p.cache, *blk, place);
-    const int page = there ? scalar_load(table + col) : -1;
-    return page < p.cache.num_pages ? page : -1;
-  };
-  auto load = [&](int v0) {
+  // ---- pages
+  const int32_t* table = p.cache.table + rt.seq * p.cache.table_stride;
+  auto entry_at = [&](int v) {   // table entry of virtual block v; -1 past the end
     int place;
-    const int page = page_at(v0 + wave, &ld_blk, &place);
-    const bool ok = page >= 0;
-    const int64_t at = ok ? page * p.cache.page_stride + (int64_t)place * kTokBlock * p.cache.token_stride : 0;
-    const uint32_t bytes = ok ? min(kTokBlock, see.len - ld_blk * kTokBlock) * ts_bytes : 0u;
-    const rsrc_t rk = make_rsrc(kbase + at * kElt, bytes), rv = make_rsrc(vbase + at * kElt, bytes);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) kr[i] = load16(rk, voff, i * kRows * ts_bytes);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) vr[i] = load16(rv, voff, i * kRows * ts_bytes);
+    const int col = page_of(p.cache, v < v_end ? see.block(v) : 0, &place);
+    return v < v_end ? table[col] : -1;
   };
-  auto store = [&](char* buf) {
-    // values that no row of the tile sees, in a block that is partly seen
-    const int j0 = ld_blk * kTokBlock;
-    const bool cut = !(j0 >= see.low || j0 + kTokBlock <= see.sinks);
+  auto page_in = [&](int entry) { return entry < p.cache.num_pages ? entry : -1; };
+  // ---- loads: this wave's tokens of a tile, all of one block
+  const int my_block = wave * kMine / kTokBlock, my_first = wave * kMine % kTokBlock;
+  const uint32_t ts_bytes = (uint32_t)p.cache.token_stride * kElt;
+  const char* kbase = static_cast<const char*>(p.cache.k) + rt.kv_head * p.cache.head_stride * kElt;
+  const char* vbase = static_cast<const char*>(p.cache.v) + rt.kv_head * p.cache.head_stride * kElt;
+  const int l_row = lane / kLanes, l_place = lane % kLanes;
+  // 16-bit caches go straight to LDS, 16 bytes per lane in lane order: the lane at
+  // a permuted place fetches the chunk that belongs there. e4m3 caches go through
+  // registers, in memory order.
+  uint32_t koff[FP8 ? 1 : kLoads], voff[2];
+  auto chunk_off = [&](int chunk) {
+    return EXACT || chunk * 16 < p.head_dim * kElt ? l_row * ts_bytes + chunk * 16 : 0x80000000u;
+  };
+  if constexpr (FP8) {
+    koff[0] = voff[0] = voff[1] = chunk_off(l_place);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) koff[i] = chunk_off(l_place ^ L::k_turn(wave * kMine + i * kRows + l_row));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) voff[i] = chunk_off(l_place ^ L::v_turn(i * kRows + l_row));   // period 4 tokens
+  }
+  u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
+  // Pages of 64 consecutive blocks, one per lane: the present group of tiles and
+  // the next, which is looked up half a group early. Where one of them is out of
+  // range, the masks of that group's tiles have to look.
+  constexpr int kGroup = 64 / kBlocks;
+  int pages, next_entries = -1;
+  bool missing = false, missed = false;   // in the present group, in the one before
+  auto enter = [&](int turn, int entries) {
+    pages = page_in(entries);
+    missed = missing;
+    missing = __any(pages < 0 && v_begin + turn * kBlocks + lane < v_end);
+  };
+  // where this wave's block of a tile lies (no bytes where there is no page)
+  struct Where {
+    int64_t at;
+    uint32_t bytes;
+  };
+  auto find = [&](int turn) {
+    const int page = __builtin_amdgcn_readlane(pages, (turn % kGroup) * kBlocks + my_block);
+    const int blk = see.block(v_begin + turn * kBlocks + my_block);
+    int place;
+    page_of(p.cache, max(0, blk), &place);
+    Where w;
+    w.at = page < 0 ? 0 : (page * p.cache.page_stride + (int64_t)place * kTokBlock * p.cache.token_stride) * kElt;
+    w.bytes = page < 0 ? 0u : min(kTokBlock, see.len - blk * kTokBlock) * ts_bytes;
+    return w;
+  };
+  const uint32_t lds_mine =
+      __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_ptr_t)lds) + wave * kMine * L::kRow;
+  auto issue_k = [&](const Where& w, int slot) {   // slot: byte offset in LDS
+    const u32x4 r = rsrc_words(kbase + w.at, w.bytes);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int t = wave * kTokBlock + i * kRows + l_row;
-      if (cut && !see.sees(j0 + i * kRows + l_row)) vr[i] = u32x4{0, 0, 0, 0};
-      if constexpr (FP8) {
-        u32x4 k[2], v[2];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          k[w / 2][2 * (w % 2)] = F::template from_fp8<false>(kr[i][w]);
-          k[w / 2][2 * (w % 2) + 1] = F::template from_fp8<true>(kr[i][w]);
-          v[w / 2][2 * (w % 2)] = PF::template from_fp8<false>(vr[i][w]);
-          v[w / 2][2 * (w % 2) + 1] = PF::template from_fp8<true>(vr[i][w]);
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          *reinterpret_cast<u32x4*>(buf + L::k_at(t, 2 * l_chunk + w)) = k[w];
-          *reinterpret_cast<u32x4*>(buf + L::kBytes + L::v_at(t, 2 * l_chunk + w)) = v[w];
-        }
-      } else {
-        *reinterpret_cast<u32x4*>(buf + L::k_at(t, l_chunk)) = kr[i];
-        *reinterpret_cast<u32x4*>(buf + L::kBytes + L::v_at(t, l_chunk)) = vr[i];
-      }
+      const uint32_t soff = (my_first + i * kRows) * ts_bytes;
+      if constexpr (FP8) kr[i] = load16(make_rsrc(kbase + w.at, w.bytes), koff[0], soff);
+      else dma_16(r, lds_mine + slot + i * 1024, koff[i], soff);
     }
+  };
+  auto issue_v = [&](const Where& w, int slot) {
+    const u32x4 r = rsrc_words(vbase + w.at, w.bytes);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t soff = (my_first + i * kRows) * ts_bytes;
+      if constexpr (FP8) vr[i] = load16(make_rsrc(vbase + w.at, w.bytes), voff[0], soff);
+      else dma_16(r, lds_mine + slot + i * 1024, voff[i & 1], soff);
+    }
+  };
+  // e4m3: widens what was loaded and writes it to its slot
+  auto widen_k = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < (FP8 ? kLoads : 0); ++i) {
+      const int t = wave * kMine + i * kRows + l_row;
+      u32x4 k[2];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        k[w / 2][2 * (w % 2)] = F::template from_fp8<false>(kr[i][w]);
+        k[w / 2][2 * (w % 2) + 1] = F::template from_fp8<true>(kr[i][w]);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) *reinterpret_cast<u32x4*>(lds + slot + L::k_at(t, 2 * l_place + w)) = k[w];
+    }
+  };
+  auto widen_v = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < (FP8 ? kLoads : 0); ++i) {
+      const int t = wave * kMine + i * kRows + l_row;
+      u32x4 v[2];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v[w / 2][2 * (w % 2)] = PF::template from_fp8<false>(vr[i][w]);
+        v[w / 2][2 * (w % 2) + 1] = PF::template from_fp8<true>(vr[i][w]);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) *reinterpret_cast<u32x4*>(lds + slot + L::v_at(t, 2 * l_place + w)) = v[w];
+    }
+  };
+  // Values that no row of the tile sees, in a block that is partly seen (the first
+  // of the window, the last with sinks), are zeroed in LDS: the turns of this
+  // wave's blocks of that kind, or -1.
+  auto turn_of = [&](int v, bool there) {
+    const int x = v - v_begin;
+    return there && x >= 0 && v < v_end && x % kBlocks == my_block ? x / kBlocks : -1;
+  };
+  const int cut_low = turn_of(see.low / kTokBlock - see.skip, see.low % kTokBlock != 0);
+  const int cut_sink = turn_of(see.sinks / kTokBlock, see.sinks % kTokBlock != 0);
+  auto cut = [&](int turn, int slot) {
+    const int j0 = see.block(v_begin + turn * kBlocks + my_block) * kTokBlock;
+    constexpr int kChunks = DP / 8;
+    for (int x = lane; x < kMine * kChunks; x += 64)
+      if (!see.sees(j0 + my_first + x / kChunks))
+        *reinterpret_cast<u32x4*>(lds + slot + wave * kMine * L::kRow + x * 16) = u32x4{0, 0, 0, 0};
   };
 
   float mref = kNegInf, sum = 0.f;
@@ -172,144 +291,223 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds, int* 
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
 
-  // transposing read: lane reads 8 bytes of token (lane % 16) / 4 of its run of
+  // ---- operand addresses, in the slots of the present tile
+  lds_char_t ka[kSteps], va[kDB];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) ka[k] = (lds_char_t)lds + L::k_at(c, 2 * k + h);
+  // transposing read: the lane reads 8 bytes of token (lane % 16) / 4 of its run of
   // four, dimensions 16 * (lane / 16 % 2) + 4 * (lane % 4)
-  const int tr_row = 4 * h + ((lane & 15) >> 2);
-  const int tr_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), tr_low = (lane & 1) * 8;
-
-  load(v_begin);
-  if (v_begin < v_end) store(lds);
-  for (int v0 = v_begin, turn = 0; v0 < v_end; v0 += kTileBlocks, turn ^= 1) {
-    const char* kt = lds + turn * 2 * L::kBytes;
-    const char* vt = kt + L::kBytes;
-    int blk[kTileBlocks];
-    bool whole = true;
 #pragma unroll
-    for (int b = 0; b < kTileBlocks; ++b) {
-      int place;
-      const int page = page_at(v0 + b, &blk[b], &place);
-      if (page < 0) blk[b] = -1;
-      const int j0 = blk[b] * kTokBlock;
-      whole = whole && blk[b] >= 0 && j0 + kTokBlock <= wave_min + 1 && (j0 >= wave_low || j0 + kTokBlock <= p.sinks);
+  for (int d = 0; d < kDB; ++d)
+    va[d] = (lds_char_t)lds + L::kV + L::v_at(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + (lane & 1) * 8;
+
+  // scores of 32 tokens, from their K operands
+  auto keys = [&](int half, u32x4 (&k)[kSteps]) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) k[i] = *(lds_u32x4_t)(ka[i] + half * 32 * L::kRow);
+  };
+  auto scores = [&](const u32x4 (&k)[kSteps]) {
+    f32x16 s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) s = F::mfma32(k[i], q[i], s);
+    return s;
+  };
+  // steps (32 tokens) of which every row of the wave sees every token
+  const int seen_low = p.window ? (max(0, wave_low) + kTokBlock - 1) / kTokBlock - see.skip - v_begin : 0;
+  const int seen_high = max(0, wave_min + 1) / kTokBlock - see.skip - v_begin;
+  const int whole_first = (max(0, seen_low) + 1) / 2;
+  const uint32_t whole_steps = (uint32_t)max(0, max(0, min(seen_high, v_end - v_begin)) / 2 - whole_first);
+  // masks the scores of step n, where a row does not see them all
+  auto mask = [&](f32x16& s, int n) {
+    const bool look = missing || missed;
+    if (!look && (uint32_t)(n - whole_first) < whole_steps) return;
+    const int v0 = v_begin + 2 * n;
+    int j0[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      j0[b] = v0 + b < v_end ? see.block(v0 + b) * kTokBlock : INT32_MAX - kTokBlock;
+      if (look && page_in(entry_at(v0 + b)) < 0) j0[b] = INT32_MAX - kTokBlock;
     }
-    __syncthreads();
-    load(v0 + kTileBlocks);
-
-    // the wave's rows may all lie before the tile's tokens
-    const bool any = see.block(v0) * kTokBlock <= wave_max;
-    if (any) {
-      f32x16 s[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          s[b] = F::mfma32(*reinterpret_cast<const u32x4*>(kt + L::k_at(32 * b + c, 2 * k + h)), q[k], s[b]);
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] *= p.scale_log2;
-      if (!whole) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = blk[2 * b + i / 8];   // registers 0-7: tokens of the first block
-            const int j = at * kTokBlock + 8 * (i / 4 % 2) + 4 * h + i % 4;
-            if (at < 0 || j > pos || (j < low && j >= p.sinks)) s[b][i] = kNegInf;
-          }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-      if (__any(top > mref + kSlack)) {
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m = fmaxf(mref, top);
-        const float f = m == kNegInf ? 1.f : exp2_of(mref - m);
-        mref = m;
-        sum *= f;
-#pragma unroll
-        for (int d = 0; d < kDB; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[d][i] *= f;
-      }
-      const float base = mref == kNegInf ? 0.f : mref;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[b][i] = exp2_of(s[b][i] - base);
-          sum += s[b][i];
-        }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {   // 16 tokens per product
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = PF::pack(s[u / 2][8 * (u % 2) + 2 * i], s[u / 2][8 * (u % 2) + 2 * i + 1]);
-#pragma unroll
-        for (int d = 0; d < kDB; ++d) {
-          u32x4 v;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int t = 16 * u + 8 * x + tr_row;
-            const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t)(vt + L::v_at(t, 4 * d + tr_chunk) + tr_low));
-            const u32x2 y = __builtin_bit_cast(u32x2, r);
-            v[2 * x] = y[0];
-            v[2 * x + 1] = y[1];
-          }
-          acc[d] = PF::mfma32(v, w, acc[d]);
-        }
-      }
+    for (int i = 0; i < 16; ++i) {
+      const int j = j0[i / 8] + 8 * (i / 4 % 2) + 4 * h + i % 4;   // registers 0-7: the first block
+      const bool hidden = (j > pos) | ((j < low) & (j >= p.sinks));
+      s[i] = hidden ? kNegInf : s[i];
     }
-    if (v0 + kTileBlocks < v_end) store(lds + (turn ^ 1) * 2 * L::kBytes);
-  }
-
-  // ---- outputs of the wave's rows, or their part
-  sum += __shfl_xor(sum, 32, 64);
-  const int64_t part_id = (int64_t)tile * p.splits + split;
-  if (parts == 1) {
-    if (live) {
-      T* dst = static_cast<T*>(p.out) + (int64_t)(q0 + qi) * p.o_ts + head * p.o_hs;
+  };
+  auto largest = [&](const f32x16& s) {
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    return top * p.scale_log2;
+  };
+  auto raise = [&](float top) {   // moves the reference maxima, if scores pass them
+    if (__any(top > mref + kSlack)) {
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float m = fmaxf(mref, top);
+      const float f = m == kNegInf ? 1.f : exp2_of(mref - m);
+      mref = m;
+      sum *= f;
 #pragma unroll
       for (int d = 0; d < kDB; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int at = 32 * d + 2 * i + 4 * h;
-          if (EXACT || at < p.head_dim)
-            *reinterpret_cast<u32x2*>(dst + at) =
-                finish<F>(f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]}, sum, p.v_scale);
-        }
+        for (int i = 0; i < 16; ++i) acc[d][i] *= f;
     }
-    return;
+  };
+  // weights of 32 tokens: two operands of 16 tokens
+  u32x4 w[2];
+  auto weigh = [&](const f32x16& s) {
+    const float base = mref == kNegInf ? 0.f : mref;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = PF::pack(exp2_of(__builtin_fmaf(s[2 * i], p.scale_log2, -base)),
+                                  exp2_of(__builtin_fmaf(s[2 * i + 1], p.scale_log2, -base)));
+      sum = PF::add_pair(x, sum);
+      w[i / 4][i % 4] = x;
+    }
+  };
+  // V operand of dimensions 32 d .., tokens 16 u .. of a half
+  auto value = [&](int half, int u, int d) {
+    u32x4 v;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const s16x4 r =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(va[d] + (half * 32 + 16 * u + 8 * x) * L::kRow));
+      const u32x2 y = __builtin_bit_cast(u32x2, r);
+      v[2 * x] = y[0];
+      v[2 * x + 1] = y[1];
+    }
+    return v;
+  };
+  // One step: scores of the next 32 tokens beside the weights of the present ones
+  // (vector operations between the matrix products), then the present outputs.
+  auto step = [&](int half, int next_half, f32x16& present, f32x16& next, int n, bool more) {
+    u32x4 k[kSteps], v[2][kDB];
+    __builtin_amdgcn_sched_barrier(0);
+    keys(next_half, k);
+    __builtin_amdgcn_sched_barrier(0);
+    next = scores(k);
+    weigh(present);
+#pragma unroll
+    for (int d = 0; d < kDB; ++d) v[0][d] = value(half, 0, d);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x002, 48 / kSteps, 0);   // vector operations
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // a matrix product
+      if (i >= kSteps / 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
+    }
+    asm volatile("" : "+v"(w[0]), "+v"(w[1]));   // not moved past the masks
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) mask(next, n + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < kDB; ++d) v[1][d] = value(half, 1, d);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int d = 0; d < kDB; ++d) acc[d] = PF::mfma32(v[u][d], w[u], acc[d]);
+    const float top = largest(next);
+    if (more) raise(top);
+  };
+
+  // tiles that some row of the wave sees
+  const int wave_blocks = wave_max < 0 ? 0 : min(see.blocks, Visible(wave_max + 1, see.low, see.sinks).blocks);
+  const int mine = max(0, min(turns, (wave_blocks - v_begin + kBlocks - 1) / kBlocks));
+
+  f32x16 s0, s1;
+  Where ahead;          // of the next tile
+  int kslot = 0;        // of the present tile; V slots alternate
+  if (turns > 0) {
+    enter(0, entry_at(v_begin + lane));
+    const Where first = find(0);
+    issue_k(first, 0);
+    ahead = find(1);
+    if constexpr (FP8) {
+      load_q();
+      widen_k(0);
+      issue_v(first, L::kV);
+      issue_k(ahead, L::kBytes);
+    } else {
+      issue_v(first, L::kV);
+      issue_k(ahead, L::kBytes);
+      load_q();
+      wait_loads<0>();
+    }
+    lds_barrier();
+    u32x4 k[kSteps];
+    keys(0, k);
+    s0 = scores(k);
+    mask(s0, 0);
+    raise(largest(s0));
   }
-  if (live) {
-    const int r = row - row0;
-    const rsrc_t out_r =
-        make_rsrc(p.partial + part_id * p.part_rows * p.head_dim, (uint32_t)(p.part_rows * p.head_dim * 4));
+  // In the turn of tile t: V of t and K of t + 1 have landed behind the barrier, and
+  // the slots of V of t - 1 and K of t - 1 are free for V of t + 1 and K of t + 2.
+  for (int t = 0; t < turns; ++t) {
+    const int vslot = L::kV + (t & 1) * L::kBytes;
+    const int next_kslot = kslot == 2 * L::kBytes ? 0 : kslot + L::kBytes;            // of tile t + 1
+    const int free_kslot = next_kslot == 2 * L::kBytes ? 0 : next_kslot + L::kBytes;  // of tile t + 2
+    if constexpr (FP8) {
+      widen_v(vslot);
+      widen_k(next_kslot);
+    } else {
+      wait_loads<0>();
+    }
+    if (t == cut_low || t == cut_sink) cut(t, vslot);
+    lds_barrier();
+    if ((t + 2) % kGroup == 0) enter(t + 2, next_entries);
+    const Where later = find(t + 2);
+    if ((t + 2) % kGroup == kGroup / 2) next_entries = entry_at(v_begin + (t + 2 + kGroup / 2) * kBlocks + lane);
+    issue_v(ahead, L::kV + ((t & 1) ^ 1) * L::kBytes);
+    issue_k(later, free_kslot);
+    ahead = later;
+    if (t < mine) {
+      if constexpr (kHalves == 2) step(0, 1, s0, s1, 2 * t, true);
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) ka[k] += next_kslot - kslot;
+      if constexpr (kHalves == 2) {
+        step(1, 0, s1, s0, 2 * t + 1, t + 1 < mine);
+      } else {
+        step(0, 0, s0, s1, t, t + 1 < mine);
+        s0 = s1;
+      }
+#pragma unroll
+      for (int d = 0; d < kDB; ++d) va[d] += (t & 1) ? -L::kBytes : L::kBytes;
+    }
+    kslot = next_kslot;
+  }
+  wait_loads<0>();   // nothing lands in LDS after this workgroup
+
+  // ---- outputs of the wave's rows, or their part
+  sum += __shfl_xor(sum, 32, 64);
+  if (!live) return;
+  if (rt.parts == 1) {
+    T* dst = static_cast<T*>(p.out) + (int64_t)(rt.q0 + qi) * p.o_ts + head * p.o_hs;
+    const float f = sum == 0.f ? 0.f : p.v_scale / sum;   // zeros where nothing was visible
 #pragma unroll
     for (int d = 0; d < kDB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const int at = 32 * d + 2 * i + 4 * h;
         if (EXACT || at < p.head_dim)
-          store16_coherent(f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]}, out_r,
-                           (uint32_t)(r * p.head_dim + at) * 4);
+          *reinterpret_cast<u32x2*>(dst + at) =
+              u32x2{F::pack(acc[d][i] * f, acc[d][i + 1] * f), F::pack(acc[d][i + 2] * f, acc[d][i + 3] * f)};
       }
-    if (h == 0) {
-      store_shared(p.stats + (part_id * p.part_rows + r) * 2, mref);
-      store_shared(p.stats + (part_id * p.part_rows + r) * 2 + 1, sum);
-    }
+    return;
   }
-  if (!workgroup_arrive_last(p.counters + tile, (uint32_t)parts, flag)) return;
-  join_parts<F>(p, tile, parts, rows, [&](int r) {
-    const int i = (row0 + r) / p.group;
-    return (int64_t)(q0 + i) * p.o_ts + (int64_t)(kv_head * p.group + row0 + r - i * p.group) * p.o_hs;
-  });
+  const int64_t r = ((int64_t)tile * p.splits + split) * p.part_rows + row - rt.row0;
+  float* dst = p.partial + r * p.head_dim;
+#pragma unroll
+  for (int d = 0; d < kDB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int at = 32 * d + 2 * i + 4 * h;
+      if (EXACT || at < p.head_dim)
+        *reinterpret_cast<f32x4*>(dst + at) = f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]};
+    }
+  if (h == 0) *reinterpret_cast<f32x2*>(p.stats + 2 * r) = f32x2{mref, sum};
 }
 
 // Two workgroups of a CU where the heads fit 128 values (two waves per SIMD); the
@@ -317,8 +515,55 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds, int* 
 template <class F, class PF, bool FP8, int DP, bool EXACT>
 __global__ void __launch_bounds__(256, DP <= 128 ? 2 : 1) attn_prefill(AttnArgs p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  __shared__ int flag;
-  prefill_body<F, PF, FP8, DP, EXACT>(p, lds, &flag);
+  prefill_body<F, PF, FP8, DP, EXACT>(p, lds);
+}
+
+// Joins the parts of the row tiles, in part order; a launch of its own, because the
+// sums of 128 rows are more than the last workgroup of a tile can read at once. A
+// thread takes four outputs of a row, `chunks` workgroups a tile.
+template <class F>
+__global__ void __launch_bounds__(256) attn_prefill_join(AttnArgs p, int chunks) {
+  const int tile = (int)(blockIdx.x / (uint32_t)chunks);
+  const RowTile rt = row_tile_of(p, tile);
+  const int x = (blockIdx.x - tile * chunks) * 256 + threadIdx.x;
+  const int quads = p.head_dim / 4;
+  const int r = (int)((uint32_t)x / (uint32_t)quads), d = 4 * (x - r * quads);
+  if (rt.parts == 1 || r >= rt.rows) return;
+  constexpr int kBatch = 16;   // parts whose loads are in flight together
+  float m = kNegInf, total = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < rt.parts; s0 += kBatch) {
+    f32x4 y[kBatch];
+    f32x2 ml[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t at = ((int64_t)tile * p.splits + min(s0 + u, rt.parts - 1)) * p.part_rows + r;
+      y[u] = *reinterpret_cast<const f32x4*>(p.partial + at * p.head_dim + d);
+      ml[u] = *reinterpret_cast<const f32x2*>(p.stats + 2 * at);
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u][0]);   // re-read last parts change nothing
+    const float base = top == kNegInf ? 0.f : top;
+    const float f0 = exp2_of(m - base);
+    total *= f0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= f0;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (s0 + u < rt.parts) {
+        const float f = exp2_of(ml[u][0] - base);
+        total += f * ml[u][1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += f * y[u][i];
+      }
+    }
+    m = top;
+  }
+  const int row = rt.row0 + r, qi = (int)((uint32_t)row / (uint32_t)p.group);
+  typename F::T* dst = static_cast<typename F::T*>(p.out) + (int64_t)(rt.q0 + qi) * p.o_ts +
+                       (int64_t)(rt.kv_head * p.group + row - qi * p.group) * p.o_hs + d;
+  *reinterpret_cast<u32x2*>(dst) = finish<F>(o, total, p.v_scale);
 }
 
 template <class F, class PF, bool FP8, int DP>
@@ -327,6 +572,10 @@ hipError_t launch_exact(const AttnArgs& a, int64_t tiles, hipStream_t s) {
   constexpr int lds = PrefillLds<DP>::kTotal;
   if (a.head_dim == DP) hipLaunchKernelGGL((attn_prefill<F, PF, FP8, DP, true>), grid, dim3(256), lds, s, a);
   else hipLaunchKernelGGL((attn_prefill<F, PF, FP8, DP, false>), grid, dim3(256), lds, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int chunks = (a.part_rows * (a.head_dim / 4) + 255) / 256;
+  hipLaunchKernelGGL((attn_prefill_join<F>), dim3((unsigned)(tiles * chunks)), dim3(256), 0, s, a, chunks);
   return hipGetLastError();
 }
 
