@@ -43,12 +43,33 @@ __device__ __forceinline__ u32x4 rsrc_words(const void* base, uint32_t bytes) {
 // the resource write zeros. Written out because the compiler waits for every such
 // load that it knows of before any LDS read that it cannot tell apart from it (it
 // cannot, for the transposing ones), which would undo the prefetch. It has no
-// register result; its arrival is waited for by hand (wait_loads).
-__device__ __forceinline__ void dma_16(u32x4 r, uint32_t dst, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+// register result; its arrival is waited for by hand (wait_loads). The wait states
+// cover M0 and resource words that a lane read has just written.
+__device__ __forceinline__ void dma_16(u32x4 r, uint32_t dst, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds"
                :
-               : "s"(dst), "v"(voff), "s"(r), "s"(soff)
+               : "s"(dst), "s"(r), "v"(voff)
                : "memory", "m0");
+}
+// Two or four of them, to dst, dst + 1024, ...: the instruction's own offset moves
+// both addresses, so load i's voff is 1024 i short.
+__device__ __forceinline__ void dma_16_run(u32x4 r, uint32_t dst, const uint32_t (&v)[2]) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
+      "buffer_load_dwordx4 %3, %1, 0 offen offset:1024 lds"
+      :
+      : "s"(dst), "s"(r), "v"(v[0]), "v"(v[1])
+      : "memory", "m0");
+}
+__device__ __forceinline__ void dma_16_run(u32x4 r, uint32_t dst, const uint32_t (&v)[4]) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
+      "buffer_load_dwordx4 %3, %1, 0 offen offset:1024 lds\n\t"
+      "buffer_load_dwordx4 %4, %1, 0 offen offset:2048 lds\n\t"
+      "buffer_load_dwordx4 %5, %1, 0 offen offset:3072 lds"
+      :
+      : "s"(dst), "s"(r), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3])
+      : "memory", "m0");
 }
 // At most N vector-memory operations of this wave are still in flight; nothing
 // moves across.
@@ -74,8 +95,9 @@ struct PrefillLds {
   static constexpr int kTile = DP <= 128 ? 64 : 32;   // tokens of a tile
   static constexpr int kRow = DP * 2;                  // bytes of a token
   static constexpr int kBytes = kTile * kRow;          // a slot
-  static constexpr int kV = 3 * kBytes;                // the first slot of V
-  static constexpr int kTotal = 5 * kBytes;
+  static constexpr int kKSlots = 3, kVSlots = 2;
+  static constexpr int kV = kKSlots * kBytes;          // the first slot of V
+  static constexpr int kTotal = (kKSlots + kVSlots) * kBytes;
   // byte place of 16-byte chunk c of token t
   static __device__ __forceinline__ int k_turn(int t) { return DP == 64 ? (t >> 1) & 7 : t & 15; }
   static __device__ __forceinline__ int v_turn(int t) { return (DP == 64 ? (t >> 1) & 1 : t & 3) << 2; }
@@ -179,65 +201,72 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   // 16-bit caches go straight to LDS, 16 bytes per lane in lane order: the lane at
   // a permuted place fetches the chunk that belongs there. e4m3 caches go through
   // registers, in memory order.
-  uint32_t koff[FP8 ? 1 : kLoads], voff[2];
-  auto chunk_off = [&](int chunk) {
-    return EXACT || chunk * 16 < p.head_dim * kElt ? l_row * ts_bytes + chunk * 16 : 0x80000000u;
-  };
-  if constexpr (FP8) {
-    koff[0] = voff[0] = voff[1] = chunk_off(l_place);
-  } else {
+  uint32_t koff[kLoads], voff[kLoads];   // of each load, within the block
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) koff[i] = chunk_off(l_place ^ L::k_turn(wave * kMine + i * kRows + l_row));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) voff[i] = chunk_off(l_place ^ L::v_turn(i * kRows + l_row));   // period 4 tokens
+  for (int i = 0; i < kLoads; ++i) {
+    const int t = my_first + i * kRows + l_row;
+    auto off = [&](int chunk) { return EXACT || chunk * 16 < p.head_dim * kElt ? t * ts_bytes + chunk * 16 : 0x80000000u; };
+    koff[i] = off(FP8 ? l_place : l_place ^ L::k_turn(wave * kMine + i * kRows + l_row));
+    voff[i] = off(FP8 ? l_place : l_place ^ L::v_turn(i * kRows + l_row));
+    // the tokens of a whole head cover at least 1024 i bytes
+    if (EXACT && !FP8) {
+      koff[i] -= i * 1024;
+      voff[i] -= i * 1024;
+    }
   }
   u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
-  // Pages of 64 consecutive blocks, one per lane: the present group of tiles and
-  // the next, which is looked up half a group early. Where one of them is out of
-  // range, the masks of that group's tiles have to look.
+  // Where 64 consecutive blocks lie, one per lane (no bytes where there is no page):
+  // the present group of tiles; the table entries of the next are fetched half a
+  // group early. Where a page is out of range, the masks of that group's tiles, and
+  // of those before it that are still in use, have to look.
   constexpr int kGroup = 64 / kBlocks;
-  int pages, next_entries = -1;
-  bool missing = false, missed = false;   // in the present group, in the one before
+  uint32_t at_low = 0, at_high = 0, at_bytes = 0;
+  int next_entries = -1;
+  bool missing = false, look = false;
   auto enter = [&](int turn, int entries) {
-    pages = page_in(entries);
-    missed = missing;
-    missing = __any(pages < 0 && v_begin + turn * kBlocks + lane < v_end);
+    const int v = v_begin + turn * kBlocks + lane, page = page_in(entries), blk = v < v_end ? see.block(v) : 0;
+    int place;
+    page_of(p.cache, blk, &place);
+    const int64_t at = (page * p.cache.page_stride + (int64_t)place * kTokBlock * p.cache.token_stride) * kElt;
+    at_low = (uint32_t)at;
+    at_high = (uint32_t)(at >> 32);
+    at_bytes = page < 0 ? 0u : min(kTokBlock, see.len - blk * kTokBlock) * ts_bytes;
+    const bool before = missing;
+    missing = __any(page < 0 && v < v_end);
+    look = missing || before;
   };
-  // where this wave's block of a tile lies (no bytes where there is no page)
+  // this wave's block of a tile
   struct Where {
-    int64_t at;
+    uint64_t at;
     uint32_t bytes;
   };
   auto find = [&](int turn) {
-    const int page = __builtin_amdgcn_readlane(pages, (turn % kGroup) * kBlocks + my_block);
-    const int blk = see.block(v_begin + turn * kBlocks + my_block);
-    int place;
-    page_of(p.cache, max(0, blk), &place);
+    const int x = (turn % kGroup) * kBlocks + my_block;
     Where w;
-    w.at = page < 0 ? 0 : (page * p.cache.page_stride + (int64_t)place * kTokBlock * p.cache.token_stride) * kElt;
-    w.bytes = page < 0 ? 0u : min(kTokBlock, see.len - blk * kTokBlock) * ts_bytes;
+    w.at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_low, x) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_high, x) << 32;
+    w.bytes = __builtin_amdgcn_readlane(at_bytes, x);
     return w;
   };
   const uint32_t lds_mine =
       __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_ptr_t)lds) + wave * kMine * L::kRow;
-  auto issue_k = [&](const Where& w, int slot) {   // slot: byte offset in LDS
-    const u32x4 r = rsrc_words(kbase + w.at, w.bytes);
+  auto issue = [&](const char* base, const Where& w, int slot, const uint32_t (&off)[kLoads],
+                   u32x4 (&regs)[FP8 ? kLoads : 1]) {   // slot: byte offset in LDS
+    if constexpr (FP8) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t soff = (my_first + i * kRows) * ts_bytes;
-      if constexpr (FP8) kr[i] = load16(make_rsrc(kbase + w.at, w.bytes), koff[0], soff);
-      else dma_16(r, lds_mine + slot + i * 1024, koff[i], soff);
+      for (int i = 0; i < kLoads; ++i) regs[i] = load16(make_rsrc(base + w.at, w.bytes), off[i], 0);
+    } else {
+      const u32x4 r = rsrc_words(base + w.at, w.bytes);
+      if constexpr (EXACT) {
+        dma_16_run(r, lds_mine + slot, off);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) dma_16(r, lds_mine + slot + i * 1024, off[i]);
+      }
     }
   };
-  auto issue_v = [&](const Where& w, int slot) {
-    const u32x4 r = rsrc_words(vbase + w.at, w.bytes);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t soff = (my_first + i * kRows) * ts_bytes;
-      if constexpr (FP8) vr[i] = load16(make_rsrc(vbase + w.at, w.bytes), voff[0], soff);
-      else dma_16(r, lds_mine + slot + i * 1024, voff[i & 1], soff);
-    }
-  };
+  auto issue_k = [&](const Where& w, int slot) { issue(kbase, w, slot, koff, kr); };
+  auto issue_v = [&](const Where& w, int slot) { issue(vbase, w, slot, voff, vr); };
   // e4m3: widens what was loaded and writes it to its slot
   auto widen_k = [&](int slot) {
 #pragma unroll
@@ -321,7 +350,6 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   const uint32_t whole_steps = (uint32_t)max(0, max(0, min(seen_high, v_end - v_begin)) / 2 - whole_first);
   // masks the scores of step n, where a row does not see them all
   auto mask = [&](f32x16& s, int n) {
-    const bool look = missing || missed;
     if (!look && (uint32_t)(n - whole_first) < whole_steps) return;
     const int v0 = v_begin + 2 * n;
     int j0[2];
@@ -356,16 +384,16 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
         for (int i = 0; i < 16; ++i) acc[d][i] *= f;
     }
   };
-  // weights of 32 tokens: two operands of 16 tokens
+  // weights of 16 tokens (u = 0, 1 of a step's 32) as an operand
   u32x4 w[2];
-  auto weigh = [&](const f32x16& s) {
+  auto weigh = [&](const f32x16& s, int u) {
     const float base = mref == kNegInf ? 0.f : mref;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t x = PF::pack(exp2_of(__builtin_fmaf(s[2 * i], p.scale_log2, -base)),
-                                  exp2_of(__builtin_fmaf(s[2 * i + 1], p.scale_log2, -base)));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = PF::pack(exp2_of(__builtin_fmaf(s[8 * u + 2 * i], p.scale_log2, -base)),
+                                  exp2_of(__builtin_fmaf(s[8 * u + 2 * i + 1], p.scale_log2, -base)));
       sum = PF::add_pair(x, sum);
-      w[i / 4][i % 4] = x;
+      w[u][i] = x;
     }
   };
   // V operand of dimensions 32 d .., tokens 16 u .. of a half
@@ -381,35 +409,47 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
     }
     return v;
   };
-  // One step: scores of the next 32 tokens beside the weights of the present ones
-  // (vector operations between the matrix products), then the present outputs.
-  auto step = [&](int half, int next_half, f32x16& present, f32x16& next, int n, bool more) {
+  // One step: scores of the next 32 tokens beside the weights of the first 16 of the
+  // present ones, then the outputs of those beside the weights of the other 16, so
+  // that vector operations stand between matrix products throughout.
+  auto step = [&](int half, int next_half, f32x16& present, f32x16& next, int number, bool more) {
     u32x4 k[kSteps], v[2][kDB];
     __builtin_amdgcn_sched_barrier(0);
     keys(next_half, k);
     __builtin_amdgcn_sched_barrier(0);
     next = scores(k);
-    weigh(present);
+    weigh(present, 0);
 #pragma unroll
     for (int d = 0; d < kDB; ++d) v[0][d] = value(half, 0, d);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x002, 48 / kSteps, 0);   // vector operations
+      __builtin_amdgcn_sched_group_barrier(0x002, 24 / kSteps, 0);   // vector operations
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // a matrix product
       if (i >= kSteps / 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
     }
-    asm volatile("" : "+v"(w[0]), "+v"(w[1]));   // not moved past the masks
+    asm volatile("" : "+v"(w[0]));   // not moved past the masks
     __builtin_amdgcn_sched_barrier(0);
-    if (more) mask(next, n + 1);
+    if (more) mask(next, number + 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int d = 0; d < kDB; ++d) v[1][d] = value(half, 1, d);
     __builtin_amdgcn_sched_barrier(0);
+    weigh(present, 1);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int d = 0; d < kDB; ++d) acc[d] = PF::mfma32(v[u][d], w[u], acc[d]);
     const float top = largest(next);
+#pragma unroll
+    for (int d = 0; d < kDB; ++d) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 24 / kDB, 0);
+    }
+#pragma unroll
+    for (int d = 0; d < kDB; ++d) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 8 / kDB, 0);
+    }
     if (more) raise(top);
   };
 
@@ -417,22 +457,26 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   const int wave_blocks = wave_max < 0 ? 0 : min(see.blocks, Visible(wave_max + 1, see.low, see.sinks).blocks);
   const int mine = max(0, min(turns, (wave_blocks - v_begin + kBlocks - 1) / kBlocks));
 
+  // ---- the line of tiles. In the turn of tile t, V of t and K of t + 1 have landed
+  // behind the barrier; V of t + 1 and K of t + 2 go to the slots that V and K of
+  // t - 1 have left.
   f32x16 s0, s1;
-  Where ahead;          // of the next tile
-  int kslot = 0;        // of the present tile; V slots alternate
+  Where ahead;                  // of tile t + 1
+  int kslot = 0, vslot = L::kV;   // of tile t
+  auto next_k = [&](int slot) { return slot == (L::kKSlots - 1) * L::kBytes ? 0 : slot + L::kBytes; };
+  auto next_v = [&](int slot) { return slot == L::kV + (L::kVSlots - 1) * L::kBytes ? L::kV : slot + L::kBytes; };
   if (turns > 0) {
     enter(0, entry_at(v_begin + lane));
-    const Where first = find(0);
-    issue_k(first, 0);
-    ahead = find(1);
+    ahead = find(0);
+    issue_k(ahead, 0);
     if constexpr (FP8) {
       load_q();
       widen_k(0);
-      issue_v(first, L::kV);
-      issue_k(ahead, L::kBytes);
-    } else {
-      issue_v(first, L::kV);
-      issue_k(ahead, L::kBytes);
+    }
+    issue_v(ahead, L::kV);
+    ahead = find(1);
+    issue_k(ahead, L::kBytes);
+    if constexpr (!FP8) {
       load_q();
       wait_loads<0>();
     }
@@ -443,30 +487,27 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
     mask(s0, 0);
     raise(largest(s0));
   }
-  // In the turn of tile t: V of t and K of t + 1 have landed behind the barrier, and
-  // the slots of V of t - 1 and K of t - 1 are free for V of t + 1 and K of t + 2.
   for (int t = 0; t < turns; ++t) {
-    const int vslot = L::kV + (t & 1) * L::kBytes;
-    const int next_kslot = kslot == 2 * L::kBytes ? 0 : kslot + L::kBytes;            // of tile t + 1
-    const int free_kslot = next_kslot == 2 * L::kBytes ? 0 : next_kslot + L::kBytes;  // of tile t + 2
+    const int kslot1 = next_k(kslot);
     if constexpr (FP8) {
       widen_v(vslot);
-      widen_k(next_kslot);
+      widen_k(kslot1);
     } else {
       wait_loads<0>();
     }
     if (t == cut_low || t == cut_sink) cut(t, vslot);
     lds_barrier();
-    if ((t + 2) % kGroup == 0) enter(t + 2, next_entries);
-    const Where later = find(t + 2);
-    if ((t + 2) % kGroup == kGroup / 2) next_entries = entry_at(v_begin + (t + 2 + kGroup / 2) * kBlocks + lane);
-    issue_v(ahead, L::kV + ((t & 1) ^ 1) * L::kBytes);
-    issue_k(later, free_kslot);
+    const int far = t + 2;
+    if (far % kGroup == 0) enter(far, next_entries);
+    const Where later = find(far);
+    if (far % kGroup == kGroup / 2) next_entries = entry_at(v_begin + (far + kGroup / 2) * kBlocks + lane);
+    issue_v(ahead, next_v(vslot));
+    issue_k(later, next_k(kslot1));
     ahead = later;
     if (t < mine) {
       if constexpr (kHalves == 2) step(0, 1, s0, s1, 2 * t, true);
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) ka[k] += next_kslot - kslot;
+      for (int k = 0; k < kSteps; ++k) ka[k] += kslot1 - kslot;
       if constexpr (kHalves == 2) {
         step(1, 0, s1, s0, 2 * t + 1, t + 1 < mine);
       } else {
@@ -474,9 +515,10 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
         s0 = s1;
       }
 #pragma unroll
-      for (int d = 0; d < kDB; ++d) va[d] += (t & 1) ? -L::kBytes : L::kBytes;
+      for (int d = 0; d < kDB; ++d) va[d] += next_v(vslot) - vslot;
     }
-    kslot = next_kslot;
+    kslot = kslot1;
+    vslot = next_v(vslot);
   }
   wait_loads<0>();   // nothing lands in LDS after this workgroup
 
