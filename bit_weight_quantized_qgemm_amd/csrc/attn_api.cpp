@@ -294,6 +294,11 @@ int run_attn(const AttnCall& g) {
   a.part_rows = pl.part_rows;
   a.splits = pl.splits;
   a.split_blocks = pl.split_blocks;
+  a.inv_group = 1.0 / a.group;
+  a.inv_kv_heads = 1.0 / a.kv_heads;
+  a.inv_seqs = 1.0 / a.num_seqs;
+  a.inv_heads = 1.0 / ((double)a.kv_heads * a.row_tiles);
+  a.inv_tiles = 1.0 / (double)pl.tiles;
   a.scale_log2 = g.scale * c->k_scale * 1.44269504088896340736f;
   a.v_scale = c->v_scale;
   if (pl.ws_bytes) {

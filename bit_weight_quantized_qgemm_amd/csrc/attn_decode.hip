@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
   // part number in equal shares
   const int heads = p.kv_heads * p.row_tiles;
   const int tiles = p.num_seqs * heads;
-  const int split = p.splits == 1 ? 0 : (int)(blockIdx.x / (uint32_t)tiles), tile = blockIdx.x - split * tiles;
-  const int seq = (int)((uint32_t)tile / (uint32_t)heads);
+  const int split = p.splits == 1 ? 0 : divide_uniform(blockIdx.x, p.inv_tiles), tile = blockIdx.x - split * tiles;
+  const int seq = divide_uniform(tile, p.inv_heads);
   const int row_tile = p.row_tiles == 1 ? 0 : (tile - seq * heads) % p.row_tiles;
   const int kv_head = p.row_tiles == 1 ? tile - seq * heads : (tile - seq * heads) / p.row_tiles;
   const int head0 = kv_head * p.group + row_tile * kDecodeRows;

@@ -73,6 +73,12 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ int32_t scalar_load(const int32_t* p) {
   return *(const __attribute__((address_space(4))) int32_t*)p;
 }
+// n / d by a precomputed 1 / d, for 0 <= n < 2^31: (n + 1/2) / d is at least 1/(2d)
+// away from every whole number, and its computed value off by less than 2^-20 / d.
+__device__ __forceinline__ int divide(int n, double inverse) { return (int)(((double)n + 0.5) * inverse); }
+__device__ __forceinline__ int divide_uniform(int n, double inverse) {
+  return __builtin_amdgcn_readfirstlane(divide(n, inverse));
+}
 // Device-scope accesses of the parts' statistics.
 __device__ __forceinline__ void store_shared(float* p, float x) {
   __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -51,6 +51,7 @@ struct AttnArgs {
   int32_t part_rows;        // rows of a tile that the partial sums hold
   int32_t splits;           // most parts of a row tile
   int32_t split_blocks;     // token blocks of a part
+  double inv_group, inv_kv_heads, inv_seqs, inv_heads, inv_tiles;   // 1 / group, ... (heads: row tiles of a sequence)
   float scale_log2;         // scale * k_scale * log2(e)
   float v_scale;
 };

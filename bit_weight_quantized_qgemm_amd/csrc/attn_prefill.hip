@@ -118,9 +118,8 @@ struct RowTile {
 // tiles, land on one XCD where there are 8 of them (or a multiple); the last rows,
 // which see most, first.
 __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& p, int tile) {
-  const uint32_t t = (uint32_t)tile / (uint32_t)p.kv_heads;
-  const int kv_head = tile - (int)t * p.kv_heads;
-  const int back = (int)(t / (uint32_t)p.num_seqs), seq = (int)t - back * p.num_seqs;
+  const int t = divide_uniform(tile, p.inv_kv_heads), kv_head = tile - t * p.kv_heads;
+  const int back = p.num_seqs == 1 ? t : divide_uniform(t, p.inv_seqs), seq = t - back * p.num_seqs;
   const int row0 = (p.row_tiles - 1 - back) * kPrefillRows;
   const int len = min(max(scalar_load(p.lens + seq), 0), p.max_len);
   const int q0 = min(max(scalar_load(p.q_start + seq), 0), p.num_tokens);
@@ -129,8 +128,8 @@ __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& p, int tile) {
   const int all_rows = new_tokens * p.group;
   const int rows = min(kPrefillRows, all_rows - row0);   // <= 0: none
   const int pos0 = len - new_tokens;
-  const int pos_min = pos0 + (int)((uint32_t)row0 / (uint32_t)p.group);
-  const int pos_max = pos0 + (int)((uint32_t)(row0 + max(1, rows) - 1) / (uint32_t)p.group);
+  const int pos_min = pos0 + divide_uniform(row0, p.inv_group);
+  const int pos_max = pos0 + divide_uniform(row0 + max(1, rows) - 1, p.inv_group);
   const Visible see(max(0, pos_max + 1), p.window ? pos_min - p.window + 1 : 0, p.window ? p.sinks : 0);
   const int parts = p.splits == 1 ? 1 : max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks);
   return RowTile{seq, kv_head, row0, rows, all_rows, q0, pos0, pos_min, pos_max, see, parts};
@@ -153,7 +152,7 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = p.num_seqs * p.kv_heads * p.row_tiles;
-  const int split = p.splits == 1 ? 0 : (int)(blockIdx.x / (uint32_t)tiles), tile = blockIdx.x - split * tiles;
+  const int split = p.splits == 1 ? 0 : divide_uniform(blockIdx.x, p.inv_tiles), tile = blockIdx.x - split * tiles;
   const RowTile rt = row_tile_of(p, tile);
   if (rt.rows <= 0 || split >= rt.parts) return;
   const Visible& see = rt.see;
@@ -163,14 +162,14 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   // ---- this lane's row, and the wave's span of positions
   const int row = rt.row0 + wave * 32 + c;
   const bool live = row < rt.all_rows;
-  const int qi = live ? (int)((uint32_t)row / (uint32_t)p.group) : 0;
+  const int qi = live ? divide(row, p.inv_group) : 0;
   const int head = rt.kv_head * p.group + (live ? row - qi * p.group : 0);
   const int pos = live ? rt.pos0 + qi : -1;
   const int low = p.window ? pos - p.window + 1 : 0;
   const int wave_rows = min(32, rt.rows - wave * 32);   // may be <= 0
-  const int wave_min = rt.pos0 + (int)((uint32_t)(rt.row0 + wave * 32) / (uint32_t)p.group);
+  const int wave_min = rt.pos0 + divide_uniform(rt.row0 + wave * 32, p.inv_group);
   const int wave_max =
-      wave_rows > 0 ? rt.pos0 + (int)((uint32_t)(rt.row0 + wave * 32 + wave_rows - 1) / (uint32_t)p.group) : -1;
+      wave_rows > 0 ? rt.pos0 + divide_uniform(rt.row0 + wave * 32 + wave_rows - 1, p.inv_group) : -1;
   const int wave_low = p.window ? wave_max - p.window + 1 : 0;   // every row of the wave sees low..min
 
   u32x4 q[kSteps];
@@ -524,18 +523,28 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
 
   // ---- outputs of the wave's rows, or their part
   sum += __shfl_xor(sum, 32, 64);
-  if (!live) return;
+  if (!live) return;   // both lanes of a row
   if (rt.parts == 1) {
     T* dst = static_cast<T*>(p.out) + (int64_t)(rt.q0 + qi) * p.o_ts + head * p.o_hs;
     const float f = sum == 0.f ? 0.f : p.v_scale / sum;   // zeros where nothing was visible
 #pragma unroll
     for (int d = 0; d < kDB; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int at = 32 * d + 2 * i + 4 * h;
-        if (EXACT || at < p.head_dim)
-          *reinterpret_cast<u32x2*>(dst + at) =
-              u32x2{F::pack(acc[d][i] * f, acc[d][i + 1] * f), F::pack(acc[d][i + 2] * f, acc[d][i + 3] * f)};
+      for (int i = 0; i < 16; i += 8) {
+        // a lane holds dimensions 4 h .. of two runs of eight; after the exchange
+        // with its partner, all eight of run h
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const u32x2 x = __builtin_bit_cast(
+              u32x2, __builtin_amdgcn_permlane32_swap(F::pack(acc[d][i + 2 * j] * f, acc[d][i + 2 * j + 1] * f),
+                                                      F::pack(acc[d][i + 4 + 2 * j] * f, acc[d][i + 5 + 2 * j] * f),
+                                                      false, false));
+          o[j] = x[0];
+          o[2 + j] = x[1];
+        }
+        const int at = 32 * d + 2 * i + 8 * h;
+        if (EXACT || at < p.head_dim) *reinterpret_cast<u32x4*>(dst + at) = o;
       }
     return;
   }
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join(AttnArgs p, int chunks)
     }
     m = top;
   }
-  const int row = rt.row0 + r, qi = (int)((uint32_t)row / (uint32_t)p.group);
+  const int row = rt.row0 + r, qi = divide(row, p.inv_group);
   typename F::T* dst = static_cast<typename F::T*>(p.out) + (int64_t)(rt.q0 + qi) * p.o_ts +
                        (int64_t)(rt.kv_head * p.group + row - qi * p.group) * p.o_hs + d;
   *reinterpret_cast<u32x2*>(dst) = finish<F>(o, total, p.v_scale);
