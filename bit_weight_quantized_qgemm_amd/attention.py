@@ -46,7 +46,9 @@ class KVCache:
         if k.stride(3) != 1:
             raise ValueError("a head's values must be contiguous")
         self.k, self.v, self.device = k, v, k.device
-        self._index = k.device.index   # of the device whose current stream the calls use
+        self._index = k.get_device()   # the calls use this device's current stream
+        torch = _torch()
+        self._int32_type, self._float32_type = torch.int32, torch.float32
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.num_pages, k.stride(0), k.stride(1), k.stride(2),
@@ -75,26 +77,29 @@ def rope_table(rows: int, rot_dim: int, theta: float = 10000.0, device=None):
     return torch.cat([angle.cos(), angle.sin()], dim=1).to(torch.float32).to(device)
 
 
-def _int32(t, name: str, device, shape):
-    if t.dtype != _torch().int32 or t.device != device or not t.is_contiguous():
+def _int32(t, name: str, cache: KVCache, shape):
+    if t.dtype is not cache._int32_type or t.get_device() != cache._index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _table(t, device):
-    if t.dim() != 2:
+def _table(t, cache: KVCache):
+    """Checks a block table; returns (pointer, columns, rows)."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [sequences][columns]")
-    _int32(t, "block_table", device, t.shape)
+    return _int32(t, "block_table", cache, shape), shape[1], shape[0]
 
 
 def _heads(t, name: str, shape, cache: KVCache, dtype):
     """Checks a [tokens][heads][head_dim] tensor (any token and head stride); returns (pointer, strides)."""
     if t.shape != shape:
         raise ValueError(f"{name} must be [tokens][heads][head_dim] = {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         raise ValueError(f"{name} must live on the cache's device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     ts, hs, one = t.stride()
     if one != 1:
@@ -110,11 +115,26 @@ def _queries(q, cache: KVCache, out):
     dt = _dtypes().get(q.dtype)
     if dt is None or dt == DT_FP8:
         raise ValueError("activations must be float16 or bfloat16")
-    qa = _heads(q, "q", shape, cache, q.dtype)
+    if q.get_device() != cache._index:
+        raise ValueError("q must live on the cache's device")
+    ts, hs, one = q.stride()
+    if one != 1:
+        raise ValueError("q: a head's values must be contiguous")
     if out is None:
         torch = _torch()
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    return shape, dt, out, qa, _heads(out, "out", shape, cache, q.dtype)
+        oa = (out.data_ptr(), shape[1] * shape[2], shape[2])
+    else:
+        oa = _heads(out, "out", shape, cache, q.dtype)
+    return shape, dt, out, (q.data_ptr(), ts, hs), oa
+
+
+def _norm(w, name: str, cache: KVCache, dtype):
+    if w is None:
+        return None
+    if w.dtype is not dtype or w.get_device() != cache._index or w.shape != (cache.head_dim,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [head_dim] tensor of q's type")
+    return w.data_ptr()
 
 
 def qk_rope_append(q, k, v, positions, cache: KVCache, block_table, rope=None, q_norm=None, k_norm=None,
@@ -125,36 +145,32 @@ def qk_rope_append(q, k, v, positions, cache: KVCache, block_table, rope=None, q
     q [tokens][q_heads][head_dim], k and v [tokens][kv_heads][head_dim], of any token and head strides (the parts of
     one fused product's output as they are); positions int32 [tokens] (negative: padding); block_table int32
     [sequences][columns]; token_seq int32 [tokens], or None when token t is sequence t's. `out` may be q."""
-    torch = _torch()
-    dev = cache.device
     shape, dt, out, qa, oa = _queries(q, cache, out)
     T, H, D = shape
-    kv_shape = (T, cache.kv_heads, D)
-    ka, va = _heads(k, "k", kv_shape, cache, q.dtype), _heads(v, "v", kv_shape, cache, q.dtype)
-    _int32(positions, "positions", dev, (T,))
-    _table(block_table, dev)
-    if token_seq is not None:
-        _int32(token_seq, "token_seq", dev, (T,))
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and (w.dtype != q.dtype or w.device != dev or w.shape != (D,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous [head_dim] tensor of q's type")
-    rows, rot = 1 << 24, 0
+    kv_shape, dtype = (T, cache.kv_heads, D), q.dtype
+    rows, rot, table = 1 << 24, 0, None
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != dev or not rope.is_contiguous():
+        if rope.dtype is not cache._float32_type or rope.dim() != 2 or rope.get_device() != cache._index or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 [positions][rot_dim] tensor")
         rows, rot = rope.shape
-    seqs, cols = block_table.shape
+        table = rope.data_ptr()
     _check(lib().qgemm_qk_rope_append(
-        *qa, *ka, *va, None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-        eps, None if rope is None else rope.data_ptr(), rows, rot, 1 if interleaved else 0, positions.data_ptr(),
-        None if token_seq is None else token_seq.data_ptr(), block_table.data_ptr(), cols, seqs, T, H, dt, cache._ref,
-        *oa, _raw_stream(cache._index)), "qgemm_qk_rope_append")
+        *qa, *_heads(k, "k", kv_shape, cache, dtype), *_heads(v, "v", kv_shape, cache, dtype),
+        _norm(q_norm, "q_norm", cache, dtype), _norm(k_norm, "k_norm", cache, dtype), eps, table, rows, rot,
+        1 if interleaved else 0, _int32(positions, "positions", cache, (T,)),
+        None if token_seq is None else _int32(token_seq, "token_seq", cache, (T,)), *_table(block_table, cache), T, H,
+        dt, cache._ref, *oa, _raw_stream(cache._index)), "qgemm_qk_rope_append")
     return out
+
+
+# Workspace sizes by shape and device: they depend on nothing else but the forced splits.
+_ws_sizes = {}
 
 
 def set_attn_splits(splits: int = 0):
     """Force the number of parts of the cache's length (0 = automatic); see include/qgemm.h."""
     _check(lib().qgemm_attn_set_splits(splits), "qgemm_attn_set_splits")
+    _ws_sizes.clear()
 
 
 def attn_decode_workspace_bytes(num_seqs: int, max_len: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -173,7 +189,13 @@ def attn_prefill_workspace_bytes(num_seqs: int, max_q: int, max_len: int, q_head
     return out.value
 
 
-def _workspace(workspace, cache, nbytes):
+def _workspace(workspace, cache, size_of, *shape):
+    key = (size_of, cache._index, *shape)
+    nbytes = _ws_sizes.get(key)
+    if nbytes is None:
+        if len(_ws_sizes) >= 4096:
+            _ws_sizes.clear()
+        nbytes = _ws_sizes[key] = size_of(*shape)
     if nbytes == 0:
         return None, 0
     ws, wsb = (workspace or _default_ws).get(nbytes, cache.device)
@@ -188,16 +210,14 @@ def attn_decode(q, cache: KVCache, block_table, seq_lens, max_len: int, scale: f
     defaults to head_dim ** -0.5. Returns q's shape and type."""
     shape, dt, out, qa, oa = _queries(q, cache, out)
     B, H, D = shape
-    dev = cache.device
-    _table(block_table, dev)
-    seqs, cols = block_table.shape
+    table, cols, seqs = _table(block_table, cache)
     if B != seqs:
         raise ValueError("q must have one row per sequence")
-    _int32(seq_lens, "seq_lens", dev, (B,))
-    ws, wsb = _workspace(workspace, cache,
-                         attn_decode_workspace_bytes(B, max_len, H, cache.kv_heads, D, window, sinks))
+    lens = _int32(seq_lens, "seq_lens", cache, (B,))
+    ws, wsb = _workspace(workspace, cache, attn_decode_workspace_bytes, B, max_len, H, cache.kv_heads, D, window,
+                         sinks)
     _check(lib().qgemm_attn_decode(
-        *qa, cache._ref, block_table.data_ptr(), cols, seq_lens.data_ptr(), B, max_len, H, dt,
+        *qa, cache._ref, table, cols, lens, B, max_len, H, dt,
         1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb, _raw_stream(cache._index)),
         "qgemm_attn_decode")
     return out
@@ -212,15 +232,13 @@ def attn_prefill(q, cache: KVCache, block_table, q_start, seq_lens, max_q: int, 
     attn_decode."""
     shape, dt, out, qa, oa = _queries(q, cache, out)
     T, H, D = shape
-    dev = cache.device
-    _table(block_table, dev)
-    seqs, cols = block_table.shape
-    _int32(q_start, "q_start", dev, (seqs + 1,))
-    _int32(seq_lens, "seq_lens", dev, (seqs,))
-    ws, wsb = _workspace(workspace, cache,
-                         attn_prefill_workspace_bytes(seqs, max_q, max_len, H, cache.kv_heads, D, window, sinks))
+    table, cols, seqs = _table(block_table, cache)
+    starts = _int32(q_start, "q_start", cache, (seqs + 1,))
+    lens = _int32(seq_lens, "seq_lens", cache, (seqs,))
+    ws, wsb = _workspace(workspace, cache, attn_prefill_workspace_bytes, seqs, max_q, max_len, H, cache.kv_heads, D,
+                         window, sinks)
     _check(lib().qgemm_attn_prefill(
-        *qa, cache._ref, block_table.data_ptr(), cols, q_start.data_ptr(), seq_lens.data_ptr(), seqs, T, max_q, max_len,
-        H, dt, 1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb,
+        *qa, cache._ref, table, cols, starts, lens, seqs, T, max_q, max_len, H, dt,
+        1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb,
         _raw_stream(cache._index)), "qgemm_attn_prefill")
     return out
