@@ -349,7 +349,7 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   const uint32_t whole_steps = (uint32_t)max(0, max(0, min(seen_high, v_end - v_begin)) / 2 - whole_first);
   // masks the scores of step n, where a row does not see them all
   auto mask = [&](f32x16& s, int n) {
-    if (!look && (uint32_t)(n - whole_first) < whole_steps) return;
+    if (__builtin_expect(!look && (uint32_t)(n - whole_first) < whole_steps, 1)) return;
     const int v0 = v_begin + 2 * n;
     int j0[2];
 #pragma unroll
@@ -371,7 +371,7 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
     return top * p.scale_log2;
   };
   auto raise = [&](float top) {   // moves the reference maxima, if scores pass them
-    if (__any(top > mref + kSlack)) {
+    if (__builtin_expect(__any(top > mref + kSlack), 0)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = fmaxf(mref, top);
       const float f = m == kNegInf ? 1.f : exp2_of(mref - m);
@@ -494,12 +494,12 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
     } else {
       wait_loads<0>();
     }
-    if (t == cut_low || t == cut_sink) cut(t, vslot);
+    if (__builtin_expect(t == cut_low || t == cut_sink, 0)) cut(t, vslot);
     lds_barrier();
     const int far = t + 2;
-    if (far % kGroup == 0) enter(far, next_entries);
+    if (__builtin_expect(far % kGroup == 0, 0)) enter(far, next_entries);
     const Where later = find(far);
-    if (far % kGroup == kGroup / 2) next_entries = entry_at(v_begin + (far + kGroup / 2) * kBlocks + lane);
+    if (__builtin_expect(far % kGroup == kGroup / 2, 0)) next_entries = entry_at(v_begin + (far + kGroup / 2) * kBlocks + lane);
     issue_v(ahead, next_v(vslot));
     issue_k(later, next_k(kslot1));
     ahead = later;
