@@ -20,6 +20,10 @@ fails loudly if its HIP build is missing.
 * ``oracle.layout``  -- an independent implementation of the repacked weight
                         blob byte layout, for byte-exact checks of the GPU repack.
 * ``oracle.compare`` -- the fp16 and bf16 output tolerance rules.
+* ``oracle.attention`` -- norm, rotation and attention over a paged cache in
+                        fp64, with the error bounds of a kernel that computes
+                        in fp32 and rounds to 16 bits; e4m3, fp16 and bf16
+                        conversions.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against values that
 do not come from the oracle itself (exact rational brute force, closed forms,
@@ -27,4 +31,4 @@ hand-derived golden files, invariants). Nothing here shares code with the HIP
 library; inputs come from the separate ``synth`` module.
 """
 
-from . import compare, layout, ref  # noqa: F401
+from . import attention, compare, layout, ref  # noqa: F401
