@@ -389,6 +389,7 @@ int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
   a.k_norm = k_norm;
   a.eps = eps;
   a.inv_dim = 1.0f / (float)c->head_dim;
+  a.inv_heads = 1.0 / (double)heads;
   a.rope = rope;
   a.rope_rows = rope_rows;
   a.rot_dim = rot_dim;

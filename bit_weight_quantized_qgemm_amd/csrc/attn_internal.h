@@ -73,6 +73,7 @@ struct AppendArgs {
   const void* q_norm;
   const void* k_norm;
   float eps, inv_dim;
+  double inv_heads;   // 1 / (q_heads + 2 kv_heads)
   const float* rope;
   int64_t rope_rows;
   int32_t rot_dim;

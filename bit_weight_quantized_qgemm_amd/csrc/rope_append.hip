@@ -51,10 +51,11 @@ __global__ void __launch_bounds__(256) rope_append(AppendArgs p) {
   constexpr int kHeads = 256 / LANES;   // heads of a workgroup
   const int lane = threadIdx.x % LANES;
   const int heads = p.q_heads + 2 * p.kv_heads;
-  const uint32_t task = blockIdx.x * (uint32_t)kHeads + threadIdx.x / LANES;
-  const uint32_t token = task / (uint32_t)heads;
-  if (token >= (uint32_t)p.num_tokens) return;   // whole heads of lanes leave together
-  int head = (int)(task - token * (uint32_t)heads);
+  // below 2^31, or in the last workgroup a little above, which wraps to a negative
+  const int task = (int)(blockIdx.x * (uint32_t)kHeads + threadIdx.x / LANES);
+  const int token = divide(task, p.inv_heads);
+  if (task < 0 || token >= p.num_tokens) return;   // whole heads of lanes leave together
+  int head = task - token * heads;
   const bool live = lane * 16 < p.head_dim;
 
   const int pos = p.positions[token];
@@ -90,6 +91,13 @@ __global__ void __launch_bounds__(256) rope_append(AppendArgs p) {
   if (live) {
     wa = *reinterpret_cast<const u32x4*>(src + ia);
     wb = *reinterpret_cast<const u32x4*>(src + ib);
+  }
+  // where a key or value goes, looked up while the head itself is on its way
+  int page = -1, place = 0;
+  if (what != Q) {
+    const int seq = p.token_seq ? p.token_seq[token] : token;
+    const int col = page_of(p.cache, pos / kTokBlock, &place);
+    if (seq >= 0 && seq < p.num_seqs && col < p.cache.table_stride) page = p.cache.table[seq * p.cache.table_stride + col];
   }
   float a[8], b[8];
   unpack8<F>(wa, a);
@@ -138,12 +146,6 @@ __global__ void __launch_bounds__(256) rope_append(AppendArgs p) {
     *reinterpret_cast<u32x4*>(dst + ib) = padding ? zero : pack8<F>(b);
     return;
   }
-  const int seq = p.token_seq ? p.token_seq[token] : (int)token;
-  if (seq < 0 || seq >= p.num_seqs) return;
-  int place;
-  const int col = page_of(p.cache, pos / kTokBlock, &place);
-  if (col >= p.cache.table_stride) return;
-  const int page = p.cache.table[seq * p.cache.table_stride + col];
   if (page < 0 || page >= p.cache.num_pages) return;
   const int64_t at = page * p.cache.page_stride + (place * kTokBlock + pos % kTokBlock) * p.cache.token_stride +
                      head * p.cache.head_stride;
