@@ -465,20 +465,16 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   auto next_k = [&](int slot) { return slot == (L::kKSlots - 1) * L::kBytes ? 0 : slot + L::kBytes; };
   auto next_v = [&](int slot) { return slot == L::kV + (L::kVSlots - 1) * L::kBytes ? L::kV : slot + L::kBytes; };
   if (turns > 0) {
-    enter(0, entry_at(v_begin + lane));
+    const int entries = entry_at(v_begin + lane);
+    load_q();   // while the entries are on their way
+    enter(0, entries);
     ahead = find(0);
     issue_k(ahead, 0);
-    if constexpr (FP8) {
-      load_q();
-      widen_k(0);
-    }
+    if constexpr (FP8) widen_k(0);
     issue_v(ahead, L::kV);
     ahead = find(1);
     issue_k(ahead, L::kBytes);
-    if constexpr (!FP8) {
-      load_q();
-      wait_loads<0>();
-    }
+    if constexpr (!FP8) wait_loads<0>();
     lds_barrier();
     u32x4 k[kSteps];
     keys(0, k);
