@@ -143,22 +143,36 @@ qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
   const int64_t blocks = visible_blocks(max_len, 1, window, sinks);
   constexpr int kStep = 2 * qg::kDecodeWaves;   // one pair of blocks for each wave
-  // Few tiles: one part per compute unit, which streams as fast as more parts and
-  // joins fewer (measured, 64/8 heads of 128, us: 1 x 131072 tokens, e4m3, 47 with
-  // 256 workgroups, 51 with 512; 4 x 16384 of one length 46, 51 with 1024). More
-  // tiles, up to two per unit: four parts per unit, because the parts of
-  // sequences of different lengths are evened out by the order in which they
-  // start (16 ragged contexts up to 8192: 59 with 1024 workgroups, 68 with 256;
-  // of one length 88 and 84). Beyond, the tiles themselves do that (64 ragged
-  // contexts up to 2048: 62 unsplit and in two parts; of one length 82 and 90).
-  // Heads above 128 values leave room for one workgroup per unit: one part each
-  // (16 contexts of 4000, 32/8 heads of 256: 85 with 256 workgroups, 101 with 1024).
-  const int64_t cus = qg::device_cu_count();
-  const int64_t fill = pl.tiles >= 2 * cus ? 0 : pl.tiles > cus / 4 && head_dim <= 128 ? 4 * cus : cus;
-  // The join reads 16 parts at a time: more of them only while each keeps four
-  // steps (4 x 8192, 16/1 heads: 15 in 16 parts, 21 in 64 of one step each).
   const int64_t steps = (blocks + kStep - 1) / kStep;
-  split(pl, blocks, std::min({fill / pl.tiles, steps, std::max<int64_t>(16, steps / 4)}), kStep, head_dim);
+  // Parts of a tile, by tiles per compute unit and steps (128 tokens) of the longest
+  // context. Joining costs about 3 us, a step of a lone workgroup 1.6. Measured on 8
+  // key-value heads of 128, 16 bits, us (one length / ragged up to it):
+  //  - up to 3 steps: unsplit (12 x 256 tokens 7.8, in two parts 9.2).
+  //  - up to a tile per four units: one part per unit, which streams as fast as more
+  //    and joins fewer (8 x 4096 in 4 parts 26 / 23, in 8 27 / 24); beyond 16 parts,
+  //    which the join reads in one go, only while each keeps four steps (4 x 8192, one
+  //    head: 15 in 16 parts, 21 in 64). Heads above 128 values leave room for one
+  //    workgroup per unit: the same up to any number of tiles (16 x 4000, 8 heads of
+  //    256: 85 in 2 parts, 101 in 8).
+  //  - up to a tile per two units: four parts per unit, whose order of starting evens
+  //    out contexts of different lengths (16 x 4096 in 8 parts 49 / 32, in 2 45 / 36);
+  //    two parts below 16 steps (16 x 1024 in 2 17 / 15, in 8 20 / 17).
+  //  - up to two tiles per unit: four parts at least, once each keeps eight steps (32
+  //    x 4096 in 4 parts 87 / 58, unsplit 80 / 64; 63 x 8192 321 / 182 and 301 / 225;
+  //    but 32 x 2048 49 / 33 and 42 / 34, 32 x 512 21 / 17 and 14 / 12); three steps
+  //    where whole tiles would leave a fifth of the units idle (40 x 1500 in 4 parts
+  //    48 / 39, unsplit 53 / 39; 40 x 3000 84 / 59 and 100 / 77).
+  //  - beyond, the tiles themselves fill the device (96 x 4096 unsplit 233 / 165, in
+  //    two parts 248 / 170).
+  const int64_t cus = qg::device_cu_count(), tiles = pl.tiles;
+  int64_t parts = 1;
+  if (steps > 3 && tiles < 2 * cus) {
+    const bool even = (tiles + cus - 1) / cus * cus * 4 <= 5 * tiles;
+    if (tiles <= cus / 4 || head_dim > 128) parts = std::min({cus / tiles, steps, std::max<int64_t>(16, steps / 4)});
+    else if (tiles <= cus / 2) parts = steps < 16 ? 2 : std::min(4 * cus / tiles, steps / 2);
+    else if (steps >= (even ? 32 : 12)) parts = std::max<int64_t>(4, 4 * cus / tiles);
+  }
+  split(pl, blocks, parts, kStep, head_dim);
   return pl;
 }
 
@@ -171,23 +185,30 @@ qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int 
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
   const int64_t blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), window, sinks);
   // Tiles of K and V hold 64 tokens (32 for heads above 128 values). One takes a
-  // workgroup that has a compute unit for itself about 1.25 us, one of two that
-  // share a unit 2.3 us, and joining s parts 6 + s / 4 us (measured; e.g. 2 x 5 new
-  // tokens on 6001, 64/8 heads of 128, 16 row tiles: 120 us unsplit, 20 in 16 parts,
-  // 23 in 32; 64 on 16384, 32 row tiles: 326, 56 in 8 parts, 52 in 16; 512 on
-  // nothing, 256 row tiles: 19, 31 in 2 parts).
+  // workgroup that has a compute unit for itself 1.25 us, and w of them that share a
+  // unit 1.15 w us together (0.9 and 0.65 w for heads of 64); a join of s parts, x MB,
+  // costs 3 + 0.08 s + 2.8 sqrt(x) us (16 parts are read at a time), with 0.45 x beyond
+  // 40 MB, where the parts leave the caches. A split has to win 5 %. Of 193 shapes
+  // (1..512 new tokens on 600..200000, 64 to 256 values, 1..16 sequences) the split
+  // that this finds is on average 2 % slower than the best of 1..256 parts (50 tokens
+  // on 20000, 64/8 heads: 58 us, best 54, unsplit 329; 12 x 40 on 12000, 32/8 heads of
+  // 64, e4m3: 99, best 95, unsplit 174).
   const int kStep = head_dim <= 128 ? 4 : 2;   // blocks of a tile of K and V
-  const int64_t steps = (blocks + kStep - 1) / kStep, cus = qg::device_cu_count();
-  const int64_t resident = head_dim <= 128 ? 2 : 1;   // workgroups of a compute unit
-  int64_t best = 1;
-  double least = 0;
-  for (int64_t s : {int64_t(1), cus / pl.tiles, resident * cus / pl.tiles}) {
-    s = std::max<int64_t>(1, std::min(s, steps));
-    const double alone = pl.tiles * s <= cus ? 1.25 : 2.3 * std::max(1.0, (double)(pl.tiles * s) / (2 * cus));
-    const double cost = (double)((steps + s - 1) / s) * alone + (s > 1 ? 6 + 0.25 * s : 0);
-    if (least == 0 || cost < least) {
-      least = cost;
-      best = s;
+  const int cus = qg::device_cu_count();
+  int best = 1;
+  if (pl.tiles <= 4 * cus) {
+    const int steps = (int)((blocks + kStep - 1) / kStep), tiles = (int)pl.tiles;
+    const double part_mb = (double)tiles * pl.part_rows * head_dim * 4e-6;
+    const double alone = head_dim <= 64 ? 0.9 : 1.25, shared = head_dim <= 64 ? 0.65 : 1.15;
+    double least = 0;
+    for (int s = 1; s <= steps && s * tiles <= 8 * cus && s <= 2 * cus; s += s < 32 ? 1 : 16) {
+      const int turns = (steps + s - 1) / s, on_unit = (tiles * s + cus - 1) / cus;
+      const double mb = part_mb * s, join = s == 1 ? 0 : 3 + 0.08 * s + std::max(2.8 * std::sqrt(mb), 0.45 * mb);
+      const double cost = turns * (on_unit == 1 ? alone : shared * on_unit) + join;
+      if (s == 1 || cost < least * (best == 1 ? 0.95 : 1)) {
+        least = cost;
+        best = s;
+      }
     }
   }
   split(pl, blocks, best, kStep, head_dim);

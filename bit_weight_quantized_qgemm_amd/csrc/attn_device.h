@@ -97,8 +97,9 @@ __device__ __forceinline__ u32x2 finish(f32x4 o, float total, float v_scale) {
 }
 
 // Joins the parts of a row tile, in part order, and writes its outputs: row r of
-// the tile to out + place(r). Called by the workgroup that arrived last, all 256
-// threads.
+// the tile to out + place(r). Called by every thread of the workgroup that arrived
+// last, with 16 parts' loads in flight together (1 x 131072 tokens in 32 parts,
+// e4m3: 46.9 us; 47.3 with 8 in flight, 59 with 32, which spill).
 template <class F, class Place>
 __device__ __forceinline__ void join_parts(const AttnArgs& p, int tile, int parts, int rows, const Place& place) {
   const int quads = p.head_dim / 4;

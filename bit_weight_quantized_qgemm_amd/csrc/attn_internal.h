@@ -41,9 +41,9 @@ struct AttnArgs {
   CacheArgs cache;
   const int32_t* lens;
   const int32_t* q_start;   // prefill
-  float* partial;           // [tile][split][rows][head_dim], then the rows' (max, sum)
-  float* stats;
-  uint32_t* counters;       // one per tile
+  float* partial;           // [tile][split][part_rows][head_dim], sums before the division
+  float* stats;             // [tile][split][part_rows] (maximum in log2 units, sum of weights)
+  uint32_t* counters;       // decode: one per tile, zero between calls
   int32_t num_seqs, kv_heads, group, head_dim;
   int32_t num_tokens, max_q, max_len;   // prefill; prefill; both
   int32_t window, sinks;

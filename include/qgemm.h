@@ -7,7 +7,9 @@
  * weights compressed to about 4 bits per element, batched decode with 1..128
  * parallel clients, memory-bound up to batch 16..32). Four weight formats,
  * a general-grid 4-bit variant (qgemm_w4g) and a bit-plane W_b A8 format
- * (qgemm_bitplane_*), both below:
+ * (qgemm_bitplane_*), both below; and, next to these products, what attention
+ * needs around a paged key-value cache (qgemm_qk_rope_append, qgemm_attn_decode,
+ * qgemm_attn_prefill; their types, shapes and strides stand with them):
  *
  *   W4A16  fp16 activations; unsigned 4-bit codes q (0..15) with an implicit
  *          zero point 8 and one fp16 scale s per group of 128 consecutive k of
@@ -392,9 +394,9 @@ int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
  * values are never used, whatever their memory holds. A sequence without visible
  * tokens (n <= 0, or no page in range) gives zeros. seq_lens is int32
  * [num_seqs] in device memory; lengths above max_len are taken as max_len.
- * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
- * to 16 bits for the matrix cores (fp16, or act_dtype's bfloat16 against a
- * bfloat16 cache), each output once to act_dtype. scale must be finite and > 0.
+ * Scores, softmax statistics and sums are fp32; each softmax weight goes to the
+ * matrix cores as two 16-bit terms (fp16, or bfloat16 against a bfloat16 cache),
+ * each output is rounded once to act_dtype. scale must be finite and > 0.
  *
  * The cache's length is split over workgroups when there are few rows; the last
  * workgroup of a row joins the parts in order, so results do not change from run
@@ -422,7 +424,9 @@ int qgemm_attn_decode(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * belong to no sequence); row numbers are bounded by num_tokens. A key or value
  * that some row of a sequence sees has to be finite: rows share the matrix
  * products of a tile, so an infinite or NaN value there may reach rows that do
- * not see it. Everything else as for qgemm_attn_decode.
+ * not see it. The softmax weights are rounded to one 16-bit term. Parts of a
+ * split length are joined by a second launch, in order. Everything else as for
+ * qgemm_attn_decode.
  */
 int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t max_len,
                                        int32_t q_heads, int32_t kv_heads, int32_t head_dim,
