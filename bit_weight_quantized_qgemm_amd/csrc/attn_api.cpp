@@ -187,8 +187,8 @@ qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int 
   // Tiles of K and V hold 64 tokens (32 for heads above 128 values). One takes a
   // workgroup that has a compute unit for itself 1.25 us, and w of them that share a
   // unit 1.15 w us together (0.9 and 0.65 w for heads of 64); a join of s parts, x MB,
-  // costs 3 + 0.08 s + 2.8 sqrt(x) us (16 parts are read at a time), with 0.45 x beyond
-  // 40 MB, where the parts leave the caches. A split has to win 5 %. Of 193 shapes
+  // costs 2 + 0.08 s + 2.8 sqrt(x) us (16 parts are read at a time), with 0.45 x beyond
+  // 40 MB, where the parts leave the caches. A split has to win 5 %. Of 197 shapes
   // (1..512 new tokens on 600..200000, 64 to 256 values, 1..16 sequences) the split
   // that this finds is on average 2 % slower than the best of 1..256 parts (50 tokens
   // on 20000, 64/8 heads: 58 us, best 54, unsplit 329; 12 x 40 on 12000, 32/8 heads of
@@ -203,7 +203,7 @@ qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int 
     double least = 0;
     for (int s = 1; s <= steps && s * tiles <= 8 * cus && s <= 2 * cus; s += s < 32 ? 1 : 16) {
       const int turns = (steps + s - 1) / s, on_unit = (tiles * s + cus - 1) / cus;
-      const double mb = part_mb * s, join = s == 1 ? 0 : 3 + 0.08 * s + std::max(2.8 * std::sqrt(mb), 0.45 * mb);
+      const double mb = part_mb * s, join = s == 1 ? 0 : 2 + 0.08 * s + std::max(2.8 * std::sqrt(mb), 0.45 * mb);
       const double cost = turns * (on_unit == 1 ? alone : shared * on_unit) + join;
       if (s == 1 || cost < least * (best == 1 ? 0.95 : 1)) {
         least = cost;
