@@ -22,7 +22,17 @@
 // The scores of the next 32 tokens are computed beside the exponentials of the
 // present ones, so the matrix and vector units of a SIMD work at the same time in
 // each of its two waves. The weights P are rounded once to 16 bits for the matrix
-// unit, and summed as rounded; statistics, sums and accumulators stay fp32.
+// unit, and summed as rounded, so that a row's weights still add up to one; that error
+// is at most about that of rounding the output. Statistics, sums and accumulators
+// stay fp32.
+//
+// Bound by the matrix unit and, with it, by power: 8192 tokens, 64/8 heads of 128,
+// bf16, take 1020 us (1075 TFLOP/s; a library product of 8192^3 reaches 1230), at
+// 1.95 GHz of 2.4 and with the matrix unit busy in 53 % of the cycles. 64 rows per
+// wave took 1058 us on a device where this takes 1026, eight waves per workgroup 1011
+// (but 512 tokens on 4096 then take 108 us instead of 77). A window of 1024 tokens
+// leaves 17 turns per workgroup: 162 us for 8192 tokens of 32/8 heads, e4m3, of which
+// a workgroup's start and end take 8 of 41 us.
 #include "attn_device.h"
 
 namespace qg {
