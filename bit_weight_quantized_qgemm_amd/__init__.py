@@ -48,6 +48,7 @@ EXPORTED_SYMBOLS = (
     "qgemm_bitplane_a8", "qgemm_bitplane_plan", "qgemm_w4g_plan", "qgemm_plan_info", "qgemm_w4a16_noalloc",
     "qgemm_qk_rope_append", "qgemm_attn_decode_workspace_bytes", "qgemm_attn_decode",
     "qgemm_attn_prefill_workspace_bytes", "qgemm_attn_prefill", "qgemm_attn_set_splits",
+    "qgemm_qk_rope_append_call", "qgemm_attn_decode_call", "qgemm_attn_prefill_call",
 )
 
 
@@ -108,6 +109,8 @@ def lib() -> ctypes.CDLL:
         L.qgemm_attn_prefill.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, i32, f32, i64, i32,
                                          vp, i64, i64, vp, ctypes.c_size_t, vp]
         L.qgemm_attn_set_splits.argtypes = [ctypes.c_int]
+        for name in ("qgemm_qk_rope_append_call", "qgemm_attn_decode_call", "qgemm_attn_prefill_call"):
+            getattr(L, name).argtypes = [ctypes.c_char_p]   # the struct's bytes
         for name in ("qgemm_qk_rope_append", "qgemm_attn_decode_workspace_bytes", "qgemm_attn_decode",
                      "qgemm_attn_prefill_workspace_bytes", "qgemm_attn_prefill", "qgemm_attn_set_splits",
                      "qgemm_packed_bytes", "qgemm_workspace_bytes", "qgemm_repack", "qgemm_w4a16",

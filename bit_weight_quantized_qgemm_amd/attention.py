@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 
 from . import DT_BF16, DT_F16, DT_FP8, Workspace, _check, _default_ws, _raw_stream, _torch, lib
 
@@ -23,6 +24,11 @@ class _CacheStruct(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+# The argument structs of the *_call entry points, packed into bytes: one argument through ctypes costs about as much
+# as all of a struct's fields.
+_attn_call = struct.Struct("@P2q2PqPP4qqP2qPNP3if").pack
+_append_call = struct.Struct("@P2qP2qP2q3Pq3P3qPP2qP4if4x").pack
 
 
 @functools.lru_cache(maxsize=None)
@@ -54,7 +60,7 @@ class KVCache:
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.num_pages, k.stride(0), k.stride(1), k.stride(2),
                                     self.page_size, self.kv_heads, self.head_dim, _dtypes()[k.dtype], self.k_scale,
                                     self.v_scale)
-        self._ref = ctypes.byref(self._struct)
+        self._address = ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype, device, k_scale: float = 1.0,
@@ -122,7 +128,10 @@ def _queries(q, cache: KVCache, out):
         raise ValueError("q: a head's values must be contiguous")
     if out is None:
         torch = _torch()
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if hs == shape[2] and ts == shape[1] * hs:   # keeps such strides
+            out = torch.empty_like(q)
+        else:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         oa = (out.data_ptr(), shape[1] * shape[2], shape[2])
     else:
         oa = _heads(out, "out", shape, cache, q.dtype)
@@ -131,7 +140,7 @@ def _queries(q, cache: KVCache, out):
 
 def _norm(w, name: str, cache: KVCache, dtype):
     if w is None:
-        return None
+        return 0
     if w.dtype is not dtype or w.get_device() != cache._index or w.shape != (cache.head_dim,) or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [head_dim] tensor of q's type")
     return w.data_ptr()
@@ -148,18 +157,23 @@ def qk_rope_append(q, k, v, positions, cache: KVCache, block_table, rope=None, q
     shape, dt, out, qa, oa = _queries(q, cache, out)
     T, H, D = shape
     kv_shape, dtype = (T, cache.kv_heads, D), q.dtype
-    rows, rot, table = 1 << 24, 0, None
+    rows, rot, rope_at = 1 << 24, 0, 0
     if rope is not None:
         if rope.dtype is not cache._float32_type or rope.dim() != 2 or rope.get_device() != cache._index or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 [positions][rot_dim] tensor")
         rows, rot = rope.shape
-        table = rope.data_ptr()
-    _check(lib().qgemm_qk_rope_append(
-        *qa, *_heads(k, "k", kv_shape, cache, dtype), *_heads(v, "v", kv_shape, cache, dtype),
-        _norm(q_norm, "q_norm", cache, dtype), _norm(k_norm, "k_norm", cache, dtype), eps, table, rows, rot,
-        1 if interleaved else 0, _int32(positions, "positions", cache, (T,)),
-        None if token_seq is None else _int32(token_seq, "token_seq", cache, (T,)), *_table(block_table, cache), T, H,
-        dt, cache._ref, *oa, _raw_stream(cache._index)), "qgemm_qk_rope_append")
+        rope_at = rope.data_ptr()
+    table, cols, seqs = _table(block_table, cache)
+    try:
+        call = _append_call(
+            *qa, *_heads(k, "k", kv_shape, cache, dtype), *_heads(v, "v", kv_shape, cache, dtype),
+            _norm(q_norm, "q_norm", cache, dtype), _norm(k_norm, "k_norm", cache, dtype), rope_at, rows,
+            _int32(positions, "positions", cache, (T,)),
+            0 if token_seq is None else _int32(token_seq, "token_seq", cache, (T,)), table, cols, seqs, T,
+            cache._address, *oa, _raw_stream(cache._index), rot, 1 if interleaved else 0, H, dt, eps)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"qk_rope_append: {e}") from None
+    _check(lib().qgemm_qk_rope_append_call(call), "qgemm_qk_rope_append")
     return out
 
 
@@ -197,7 +211,7 @@ def _workspace(workspace, cache, size_of, *shape):
             _ws_sizes.clear()
         nbytes = _ws_sizes[key] = size_of(*shape)
     if nbytes == 0:
-        return None, 0
+        return 0, 0
     ws, wsb = (workspace or _default_ws).get(nbytes, cache.device)
     return ws.data_ptr(), wsb
 
@@ -216,10 +230,12 @@ def attn_decode(q, cache: KVCache, block_table, seq_lens, max_len: int, scale: f
     lens = _int32(seq_lens, "seq_lens", cache, (B,))
     ws, wsb = _workspace(workspace, cache, attn_decode_workspace_bytes, B, max_len, H, cache.kv_heads, D, window,
                          sinks)
-    _check(lib().qgemm_attn_decode(
-        *qa, cache._ref, table, cols, lens, B, max_len, H, dt,
-        1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb, _raw_stream(cache._index)),
-        "qgemm_attn_decode")
+    try:
+        call = _attn_call(*qa, cache._address, table, cols, 0, lens, B, B, 1, max_len, window, *oa, ws, wsb,
+                          _raw_stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"attn_decode: {e}") from None
+    _check(lib().qgemm_attn_decode_call(call), "qgemm_attn_decode")
     return out
 
 
@@ -237,8 +253,10 @@ def attn_prefill(q, cache: KVCache, block_table, q_start, seq_lens, max_q: int, 
     lens = _int32(seq_lens, "seq_lens", cache, (seqs,))
     ws, wsb = _workspace(workspace, cache, attn_prefill_workspace_bytes, seqs, max_q, max_len, H, cache.kv_heads, D,
                          window, sinks)
-    _check(lib().qgemm_attn_prefill(
-        *qa, cache._ref, table, cols, starts, lens, seqs, T, max_q, max_len, H, dt,
-        1.0 / math.sqrt(D) if scale is None else scale, window, sinks, *oa, ws, wsb,
-        _raw_stream(cache._index)), "qgemm_attn_prefill")
+    try:
+        call = _attn_call(*qa, cache._address, table, cols, starts, lens, seqs, T, max_q, max_len, window, *oa, ws, wsb,
+                          _raw_stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"attn_prefill: {e}") from None
+    _check(lib().qgemm_attn_prefill_call(call), "qgemm_attn_prefill")
     return out

@@ -225,64 +225,47 @@ int check_attn_shape(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t
   return check_heads(q_heads, kv_heads);
 }
 
-struct AttnCall {
-  const void* q;
-  int64_t q_ts, q_hs;
-  const qgemm_kv_cache* cache;
-  const int32_t* table;
-  int64_t table_stride;
-  const int32_t* q_start;   // prefill only
-  const int32_t* lens;
-  int64_t num_seqs, num_tokens, max_q, max_len;
-  int32_t q_heads, act_dtype;
-  float scale;
-  int64_t window;
-  int32_t sinks;
-  void* out;
-  int64_t o_ts, o_hs;
-  void* ws;
-  size_t ws_bytes;
-  void* stream;
-  bool prefill;
-};
-
-int run_attn(const AttnCall& g) {
+int run_attn(const qgemm_attn_call& g, bool prefill) {
   const qgemm_kv_cache* c = g.cache;
+  const int64_t num_tokens = prefill ? g.num_tokens : g.num_seqs, max_q = prefill ? g.max_q : 1;
+  const int32_t* q_start = prefill ? g.q_start : nullptr;
   if (!c) return QGEMM_ERR_NULL;
   if (!valid_act(g.act_dtype)) return QGEMM_ERR_RANGE;
   int st = check_attn_shape(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
   if (st) return st;
-  if (g.num_tokens < 0 || g.num_tokens > kMaxTokens || g.max_q < 0 || g.max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
+  if (num_tokens < 0 || num_tokens > kMaxTokens || max_q < 0 || max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
   st = check_cache(c, g.act_dtype);
   if (st) return st;
   if (!positive(g.scale) || !positive(g.scale * c->k_scale)) return QGEMM_ERR_RANGE;
-  if (g.num_seqs == 0 || g.num_tokens == 0 || g.max_q == 0) return QGEMM_OK;
-  if (!g.q || !g.out || !g.lens || (!g.table && g.table_stride > 0) || (g.prefill && !g.q_start)) return QGEMM_ERR_NULL;
-  if (!aligned(g.q, 16) || !aligned(g.out, 16) || !aligned(g.lens, 4) || !aligned(g.table, 4) || !aligned(g.q_start, 4))
+  if (g.num_seqs == 0 || num_tokens == 0 || max_q == 0) return QGEMM_OK;
+  if (!g.q || !g.out || !g.seq_lens || (!g.block_table && g.table_stride > 0) || (prefill && !q_start))
+    return QGEMM_ERR_NULL;
+  if (!aligned(g.q, 16) || !aligned(g.out, 16) || !aligned(g.seq_lens, 4) || !aligned(g.block_table, 4) ||
+      !aligned(q_start, 4))
     return QGEMM_ERR_ALIGN;
-  if (!valid_strides(g.q_ts, g.q_hs, g.q_heads, c->head_dim) ||
-      !valid_out_strides(g.num_tokens, g.o_ts, g.o_hs, g.q_heads, c->head_dim))
+  if (!valid_strides(g.q_token_stride, g.q_head_stride, g.q_heads, c->head_dim) ||
+      !valid_out_strides(num_tokens, g.out_token_stride, g.out_head_stride, g.q_heads, c->head_dim))
     return QGEMM_ERR_ALIGN;
   if (g.table_stride < 0 || g.table_stride > kMaxLen || g.max_len > g.table_stride * c->page_size)
     return QGEMM_ERR_SHAPE;
 
   const qg::AttnPlan pl =
-      g.prefill ? prefill_plan(g.num_seqs, g.max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks)
-                : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
+      prefill ? prefill_plan(g.num_seqs, max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks)
+              : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
   if (pl.tiles * pl.splits > INT32_MAX) return QGEMM_ERR_SHAPE;
   if (pl.ws_bytes > 0) {
-    if (!g.ws) return QGEMM_ERR_NULL;
-    if (g.ws_bytes < pl.ws_bytes) return QGEMM_ERR_WORKSPACE;
-    if (!aligned(g.ws, 16)) return QGEMM_ERR_ALIGN;
+    if (!g.workspace) return QGEMM_ERR_NULL;
+    if (g.workspace_bytes < pl.ws_bytes) return QGEMM_ERR_WORKSPACE;
+    if (!aligned(g.workspace, 16)) return QGEMM_ERR_ALIGN;
   }
-  const Extent out = extent3(g.out, g.num_tokens, g.o_ts, g.q_heads, g.o_hs, c->head_dim);
-  const Extent others[] = {extent3(g.q, g.num_tokens, g.q_ts, g.q_heads, g.q_hs, c->head_dim),
+  const Extent out = extent3(g.out, num_tokens, g.out_token_stride, g.q_heads, g.out_head_stride, c->head_dim);
+  const Extent others[] = {extent3(g.q, num_tokens, g.q_token_stride, g.q_heads, g.q_head_stride, c->head_dim),
                            cache_extent(c, c->k),
                            cache_extent(c, c->v),
-                           extent(g.table, g.num_seqs * g.table_stride, 4),
-                           extent(g.lens, g.num_seqs, 4),
-                           extent(g.q_start, g.num_seqs + 1, 4),
-                           extent(pl.ws_bytes ? g.ws : nullptr, (int64_t)pl.ws_bytes, 1)};
+                           extent(g.block_table, g.num_seqs * g.table_stride, 4),
+                           extent(g.seq_lens, g.num_seqs, 4),
+                           extent(q_start, g.num_seqs + 1, 4),
+                           extent(pl.ws_bytes ? g.workspace : nullptr, (int64_t)pl.ws_bytes, 1)};
   for (const Extent& e : others)
     if (overlap(out, e)) return QGEMM_ERR_ALIAS;
   if (pl.ws_bytes)
@@ -294,19 +277,19 @@ int run_attn(const AttnCall& g) {
   qg::AttnArgs a{};
   a.q = g.q;
   a.out = g.out;
-  a.q_ts = g.q_ts;
-  a.q_hs = g.q_hs;
-  a.o_ts = g.o_ts;
-  a.o_hs = g.o_hs;
-  a.cache = cache_args(c, g.table, g.table_stride);
-  a.lens = g.lens;
-  a.q_start = g.q_start;
+  a.q_ts = g.q_token_stride;
+  a.q_hs = g.q_head_stride;
+  a.o_ts = g.out_token_stride;
+  a.o_hs = g.out_head_stride;
+  a.cache = cache_args(c, g.block_table, g.table_stride);
+  a.lens = g.seq_lens;
+  a.q_start = q_start;
   a.num_seqs = (int32_t)g.num_seqs;
   a.kv_heads = c->kv_heads;
   a.group = g.q_heads / c->kv_heads;
   a.head_dim = c->head_dim;
-  a.num_tokens = (int32_t)g.num_tokens;
-  a.max_q = (int32_t)g.max_q;
+  a.num_tokens = (int32_t)num_tokens;
+  a.max_q = (int32_t)max_q;
   a.max_len = (int32_t)g.max_len;
   // a window beyond every position is none; sinks beyond max_len are all tokens
   a.window = g.window >= g.max_len ? 0 : (int32_t)g.window;
@@ -323,68 +306,60 @@ int run_attn(const AttnCall& g) {
   a.scale_log2 = g.scale * c->k_scale * 1.44269504088896340736f;
   a.v_scale = c->v_scale;
   if (pl.ws_bytes) {
-    char* ws = static_cast<char*>(g.ws);
+    char* ws = static_cast<char*>(g.workspace);
     a.counters = reinterpret_cast<uint32_t*>(ws);
     a.stats = reinterpret_cast<float*>(ws + pl.stats_offset);
     a.partial = reinterpret_cast<float*>(ws + pl.partial_offset);
   }
   const bool bf16 = g.act_dtype == QGEMM_DT_BF16, fp8 = c->dtype == QGEMM_DT_FP8;
   hipStream_t s = static_cast<hipStream_t>(g.stream);
-  const hipError_t e = g.prefill ? qg::launch_attn_prefill(a, bf16, fp8, pl.tiles, s)
-                                 : qg::launch_attn_decode(a, bf16, fp8, pl.tiles, s);
+  const hipError_t e = prefill ? qg::launch_attn_prefill(a, bf16, fp8, pl.tiles, s)
+                               : qg::launch_attn_decode(a, bf16, fp8, pl.tiles, s);
   if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
   return QGEMM_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
-                         int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
-                         int64_t v_head_stride, const void* q_norm, const void* k_norm, float eps, const float* rope,
-                         int64_t rope_rows, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
-                         const int32_t* token_seq, const int32_t* block_table, int64_t table_stride, int64_t num_seqs,
-                         int64_t num_tokens, int32_t q_heads, int32_t act_dtype, const qgemm_kv_cache* cache,
-                         void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, void* stream) {
-  const qgemm_kv_cache* c = cache;
+int run_append(const qgemm_append_call& g) {
+  const qgemm_kv_cache* c = g.cache;
   if (!c) return QGEMM_ERR_NULL;
-  if (!valid_act(act_dtype) || (interleaved != 0 && interleaved != 1)) return QGEMM_ERR_RANGE;
-  if (num_seqs < 0 || num_seqs > kMaxSeqs || num_tokens < 0 || num_tokens > kMaxTokens) return QGEMM_ERR_SHAPE;
-  int st = check_cache(c, act_dtype);
+  if (!valid_act(g.act_dtype) || (g.interleaved != 0 && g.interleaved != 1)) return QGEMM_ERR_RANGE;
+  if (g.num_seqs < 0 || g.num_seqs > kMaxSeqs || g.num_tokens < 0 || g.num_tokens > kMaxTokens) return QGEMM_ERR_SHAPE;
+  int st = check_cache(c, g.act_dtype);
   if (st) return st;
-  st = check_heads(q_heads, c->kv_heads);
+  st = check_heads(g.q_heads, c->kv_heads);
   if (st) return st;
   // 32-bit task numbers over the tokens' heads
-  const int64_t heads = (int64_t)q_heads + 2 * c->kv_heads;
-  if (num_tokens * heads >= (int64_t(1) << 31)) return QGEMM_ERR_SHAPE;
-  if (rot_dim < 0 || rot_dim > c->head_dim || rot_dim % 16 != 0) return QGEMM_ERR_SHAPE;
-  if (rope_rows < 0 || rope_rows > kMaxLen) return QGEMM_ERR_SHAPE;
-  if (table_stride < 0 || table_stride > kMaxLen) return QGEMM_ERR_SHAPE;
-  if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.f)) return QGEMM_ERR_RANGE;
-  if (num_tokens == 0) return QGEMM_OK;
-  if (!q || !k || !v || !q_out || !positions || !block_table || (rot_dim > 0 && !rope)) return QGEMM_ERR_NULL;
-  for (const void* p : {q, k, v, q_norm, k_norm, (const void*)rope, (const void*)q_out})
+  const int64_t heads = (int64_t)g.q_heads + 2 * c->kv_heads;
+  if (g.num_tokens * heads >= (int64_t(1) << 31)) return QGEMM_ERR_SHAPE;
+  if (g.rot_dim < 0 || g.rot_dim > c->head_dim || g.rot_dim % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (g.rope_rows < 0 || g.rope_rows > kMaxLen) return QGEMM_ERR_SHAPE;
+  if (g.table_stride < 0 || g.table_stride > kMaxLen) return QGEMM_ERR_SHAPE;
+  if ((g.q_norm || g.k_norm) && !(std::isfinite(g.eps) && g.eps >= 0.f)) return QGEMM_ERR_RANGE;
+  if (g.num_tokens == 0) return QGEMM_OK;
+  if (!g.q || !g.k || !g.v || !g.q_out || !g.positions || !g.block_table || (g.rot_dim > 0 && !g.rope))
+    return QGEMM_ERR_NULL;
+  for (const void* p : {g.q, g.k, g.v, g.q_norm, g.k_norm, (const void*)g.rope, (const void*)g.q_out})
     if (!aligned(p, 16)) return QGEMM_ERR_ALIGN;
-  if (!aligned(positions, 4) || !aligned(token_seq, 4) || !aligned(block_table, 4)) return QGEMM_ERR_ALIGN;
-  if (!valid_strides(q_token_stride, q_head_stride, q_heads, c->head_dim) ||
-      !valid_strides(k_token_stride, k_head_stride, c->kv_heads, c->head_dim) ||
-      !valid_strides(v_token_stride, v_head_stride, c->kv_heads, c->head_dim) ||
-      !valid_out_strides(num_tokens, qo_token_stride, qo_head_stride, q_heads, c->head_dim))
+  if (!aligned(g.positions, 4) || !aligned(g.token_seq, 4) || !aligned(g.block_table, 4)) return QGEMM_ERR_ALIGN;
+  if (!valid_strides(g.q_token_stride, g.q_head_stride, g.q_heads, c->head_dim) ||
+      !valid_strides(g.k_token_stride, g.k_head_stride, c->kv_heads, c->head_dim) ||
+      !valid_strides(g.v_token_stride, g.v_head_stride, c->kv_heads, c->head_dim) ||
+      !valid_out_strides(g.num_tokens, g.out_token_stride, g.out_head_stride, g.q_heads, c->head_dim))
     return QGEMM_ERR_ALIGN;
   const int64_t D = c->head_dim;
-  const Extent eq = extent3(q, num_tokens, q_token_stride, q_heads, q_head_stride, D);
-  const Extent out = extent3(q_out, num_tokens, qo_token_stride, q_heads, qo_head_stride, D);
+  const Extent eq = extent3(g.q, g.num_tokens, g.q_token_stride, g.q_heads, g.q_head_stride, D);
+  const Extent out = extent3(g.q_out, g.num_tokens, g.out_token_stride, g.q_heads, g.out_head_stride, D);
   const Extent kc = cache_extent(c, c->k), vc = cache_extent(c, c->v);
-  const Extent in[] = {extent3(k, num_tokens, k_token_stride, c->kv_heads, k_head_stride, D),
-                       extent3(v, num_tokens, v_token_stride, c->kv_heads, v_head_stride, D),
-                       extent(q_norm, D, 2),
-                       extent(k_norm, D, 2),
-                       extent(rope, rope_rows * rot_dim, 4),
-                       extent(positions, num_tokens, 4),
-                       extent(token_seq, num_tokens, 4),
-                       extent(block_table, num_seqs * table_stride, 4)};
-  const bool in_place = q_out == q && qo_token_stride == q_token_stride && qo_head_stride == q_head_stride;
+  const Extent in[] = {extent3(g.k, g.num_tokens, g.k_token_stride, c->kv_heads, g.k_head_stride, D),
+                       extent3(g.v, g.num_tokens, g.v_token_stride, c->kv_heads, g.v_head_stride, D),
+                       extent(g.q_norm, D, 2),
+                       extent(g.k_norm, D, 2),
+                       extent(g.rope, g.rope_rows * g.rot_dim, 4),
+                       extent(g.positions, g.num_tokens, 4),
+                       extent(g.token_seq, g.num_tokens, 4),
+                       extent(g.block_table, g.num_seqs * g.table_stride, 4)};
+  const bool in_place =
+      g.q_out == g.q && g.out_token_stride == g.q_token_stride && g.out_head_stride == g.q_head_stride;
   if (!in_place && overlap(out, eq)) return QGEMM_ERR_ALIAS;
   // the parts of one fused product interleave in memory: an in-place q_out may
   // span k and v without touching them, so only a separate q_out is checked
@@ -395,40 +370,88 @@ int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
   if (st) return st;
 
   qg::AppendArgs a{};
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_ts = q_token_stride;
-  a.q_hs = q_head_stride;
-  a.k_ts = k_token_stride;
-  a.k_hs = k_head_stride;
-  a.v_ts = v_token_stride;
-  a.v_hs = v_head_stride;
-  a.qo_ts = qo_token_stride;
-  a.qo_hs = qo_head_stride;
-  a.q_norm = q_norm;
-  a.k_norm = k_norm;
-  a.eps = eps;
+  a.q = g.q;
+  a.k = g.k;
+  a.v = g.v;
+  a.q_ts = g.q_token_stride;
+  a.q_hs = g.q_head_stride;
+  a.k_ts = g.k_token_stride;
+  a.k_hs = g.k_head_stride;
+  a.v_ts = g.v_token_stride;
+  a.v_hs = g.v_head_stride;
+  a.qo_ts = g.out_token_stride;
+  a.qo_hs = g.out_head_stride;
+  a.q_norm = g.q_norm;
+  a.k_norm = g.k_norm;
+  a.eps = g.eps;
   a.inv_dim = 1.0f / (float)c->head_dim;
   a.inv_heads = 1.0 / (double)heads;
-  a.rope = rope;
-  a.rope_rows = rope_rows;
-  a.rot_dim = rot_dim;
-  a.positions = positions;
-  a.token_seq = token_seq;
-  a.cache = cache_args(c, block_table, table_stride);
-  a.num_seqs = (int32_t)num_seqs;
-  a.num_tokens = (int32_t)num_tokens;
-  a.q_heads = q_heads;
+  a.rope = g.rope;
+  a.rope_rows = g.rope_rows;
+  a.rot_dim = g.rot_dim;
+  a.positions = g.positions;
+  a.token_seq = g.token_seq;
+  a.cache = cache_args(c, g.block_table, g.table_stride);
+  a.num_seqs = (int32_t)g.num_seqs;
+  a.num_tokens = (int32_t)g.num_tokens;
+  a.q_heads = g.q_heads;
   a.kv_heads = c->kv_heads;
   a.head_dim = c->head_dim;
-  a.q_out = q_out;
+  a.q_out = g.q_out;
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;
-  const hipError_t e = qg::launch_append(a, act_dtype == QGEMM_DT_BF16, c->dtype == QGEMM_DT_FP8, interleaved != 0,
-                                         static_cast<hipStream_t>(stream));
+  const hipError_t e = qg::launch_append(a, g.act_dtype == QGEMM_DT_BF16, c->dtype == QGEMM_DT_FP8,
+                                         g.interleaved != 0, static_cast<hipStream_t>(g.stream));
   if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
   return QGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qgemm_qk_rope_append_call(const qgemm_append_call* call) {
+  return call ? run_append(*call) : QGEMM_ERR_NULL;
+}
+
+int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                         int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                         int64_t v_head_stride, const void* q_norm, const void* k_norm, float eps, const float* rope,
+                         int64_t rope_rows, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                         const int32_t* token_seq, const int32_t* block_table, int64_t table_stride, int64_t num_seqs,
+                         int64_t num_tokens, int32_t q_heads, int32_t act_dtype, const qgemm_kv_cache* cache,
+                         void* q_out, int64_t qo_token_stride, int64_t qo_head_stride, void* stream) {
+  qgemm_append_call g{};
+  g.q = q;
+  g.q_token_stride = q_token_stride;
+  g.q_head_stride = q_head_stride;
+  g.k = k;
+  g.k_token_stride = k_token_stride;
+  g.k_head_stride = k_head_stride;
+  g.v = v;
+  g.v_token_stride = v_token_stride;
+  g.v_head_stride = v_head_stride;
+  g.q_norm = q_norm;
+  g.k_norm = k_norm;
+  g.rope = rope;
+  g.rope_rows = rope_rows;
+  g.positions = positions;
+  g.token_seq = token_seq;
+  g.block_table = block_table;
+  g.table_stride = table_stride;
+  g.num_seqs = num_seqs;
+  g.num_tokens = num_tokens;
+  g.cache = cache;
+  g.q_out = q_out;
+  g.out_token_stride = qo_token_stride;
+  g.out_head_stride = qo_head_stride;
+  g.stream = stream;
+  g.rot_dim = rot_dim;
+  g.interleaved = interleaved;
+  g.q_heads = q_heads;
+  g.act_dtype = act_dtype;
+  g.eps = eps;
+  return run_append(g);
 }
 
 int qgemm_attn_decode_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t kv_heads,
@@ -440,14 +463,37 @@ int qgemm_attn_decode_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t
   return QGEMM_OK;
 }
 
+int qgemm_attn_decode_call(const qgemm_attn_call* call) {
+  return call ? run_attn(*call, false) : QGEMM_ERR_NULL;
+}
+
 int qgemm_attn_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, const qgemm_kv_cache* cache,
                       const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, int64_t num_seqs,
                       int64_t max_len, int32_t q_heads, int32_t act_dtype, float scale, int64_t window, int32_t sinks,
                       void* out, int64_t out_token_stride, int64_t out_head_stride, void* workspace,
                       size_t workspace_bytes, void* stream) {
-  return run_attn({q, q_token_stride, q_head_stride, cache, block_table, table_stride, nullptr, seq_lens, num_seqs,
-                   num_seqs, 1, max_len, q_heads, act_dtype, scale, window, sinks, out, out_token_stride,
-                   out_head_stride, workspace, workspace_bytes, stream, false});
+  qgemm_attn_call g{};
+  g.q = q;
+  g.q_token_stride = q_token_stride;
+  g.q_head_stride = q_head_stride;
+  g.cache = cache;
+  g.block_table = block_table;
+  g.table_stride = table_stride;
+  g.seq_lens = seq_lens;
+  g.num_seqs = num_seqs;
+  g.max_len = max_len;
+  g.window = window;
+  g.out = out;
+  g.out_token_stride = out_token_stride;
+  g.out_head_stride = out_head_stride;
+  g.workspace = workspace;
+  g.workspace_bytes = workspace_bytes;
+  g.stream = stream;
+  g.q_heads = q_heads;
+  g.act_dtype = act_dtype;
+  g.sinks = sinks;
+  g.scale = scale;
+  return run_attn(g, false);
 }
 
 int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t max_len, int32_t q_heads,
@@ -463,15 +509,41 @@ int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t 
   return QGEMM_OK;
 }
 
+int qgemm_attn_prefill_call(const qgemm_attn_call* call) {
+  return call ? run_attn(*call, true) : QGEMM_ERR_NULL;
+}
+
 int qgemm_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const qgemm_kv_cache* cache,
                        const int32_t* block_table, int64_t table_stride, const int32_t* q_start,
                        const int32_t* seq_lens, int64_t num_seqs, int64_t num_tokens, int64_t max_q, int64_t max_len,
                        int32_t q_heads, int32_t act_dtype, float scale, int64_t window, int32_t sinks, void* out,
                        int64_t out_token_stride, int64_t out_head_stride, void* workspace, size_t workspace_bytes,
                        void* stream) {
-  return run_attn({q, q_token_stride, q_head_stride, cache, block_table, table_stride, q_start, seq_lens, num_seqs,
-                   num_tokens, max_q, max_len, q_heads, act_dtype, scale, window, sinks, out, out_token_stride,
-                   out_head_stride, workspace, workspace_bytes, stream, true});
+  qgemm_attn_call g{};
+  g.q = q;
+  g.q_token_stride = q_token_stride;
+  g.q_head_stride = q_head_stride;
+  g.cache = cache;
+  g.block_table = block_table;
+  g.table_stride = table_stride;
+  g.q_start = q_start;
+  g.seq_lens = seq_lens;
+  g.num_seqs = num_seqs;
+  g.num_tokens = num_tokens;
+  g.max_q = max_q;
+  g.max_len = max_len;
+  g.window = window;
+  g.out = out;
+  g.out_token_stride = out_token_stride;
+  g.out_head_stride = out_head_stride;
+  g.workspace = workspace;
+  g.workspace_bytes = workspace_bytes;
+  g.stream = stream;
+  g.q_heads = q_heads;
+  g.act_dtype = act_dtype;
+  g.sinks = sinks;
+  g.scale = scale;
+  return run_attn(g, true);
 }
 
 int qgemm_attn_set_splits(int splits) {

@@ -440,6 +440,59 @@ int qgemm_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
                        size_t workspace_bytes, void* stream);
 
 /*
+ * The three calls above with their arguments in one struct, field by argument of
+ * the same name (qo_* of the append call are out_* here): for bindings in which
+ * every argument of a call costs time (30 of them 3 us through ctypes, a struct 1). The
+ * struct is read before the call returns. q_start, num_tokens and max_q belong to
+ * the prefill call; the decode call ignores them. A NULL struct is QGEMM_ERR_NULL.
+ */
+typedef struct qgemm_attn_call {
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const qgemm_kv_cache* cache;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* q_start;
+  const int32_t* seq_lens;
+  int64_t num_seqs, num_tokens, max_q, max_len;
+  int64_t window;
+  void* out;
+  int64_t out_token_stride, out_head_stride;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+  int32_t q_heads, act_dtype, sinks;
+  float scale;
+} qgemm_attn_call;
+
+typedef struct qgemm_append_call {
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  const void* v;
+  int64_t v_token_stride, v_head_stride;
+  const void* q_norm;
+  const void* k_norm;
+  const float* rope;
+  int64_t rope_rows;
+  const int32_t* positions;
+  const int32_t* token_seq;
+  const int32_t* block_table;
+  int64_t table_stride, num_seqs, num_tokens;
+  const qgemm_kv_cache* cache;
+  void* q_out;
+  int64_t out_token_stride, out_head_stride;
+  void* stream;
+  int32_t rot_dim, interleaved, q_heads, act_dtype;
+  float eps;
+} qgemm_append_call;
+
+int qgemm_qk_rope_append_call(const qgemm_append_call* call);
+int qgemm_attn_decode_call(const qgemm_attn_call* call);
+int qgemm_attn_prefill_call(const qgemm_attn_call* call);
+
+/*
  * Force the number of parts into which later attention calls of this process
  * split the cache's length (1..1024; 0: automatic). For tests and tuning, like
  * qgemm_set_plan_override; affects the attention workspace queries too.

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import bit_weight_quantized_qgemm_amd as qg
+from bit_weight_quantized_qgemm_amd import attention
 from bit_weight_quantized_qgemm_amd.attention import _CacheStruct
 
 OK, NULL, SHAPE, ALIGN, WS, RANGE, ALIAS, HIP, DEV = 0, -1, -2, -3, -4, -6, -7, -8, -9
@@ -193,3 +194,67 @@ def test_cache_binding_refuses_tensors_that_do_not_fit():
                 lambda: qg.KVCache(k, k.transpose(0, 1).contiguous().transpose(0, 1))):
         with pytest.raises(ValueError):
             bad()
+
+
+def _attn_struct(cache=None, **kw):
+    a = dict(q=Q, qts=64 * 128, qhs=128, table=TABLE, cols=64, start=START, lens=LENS, seqs=4, tokens=40, max_q=20,
+             max_len=1000, heads=64, act=F16, scale=0.1, window=0, sinks=0, out=OUT, ots=64 * 128, ohs=128, ws=WSP,
+             wsb=1 << 30)
+    a.update(kw)
+    c = cache if cache is not None else _cache()
+    return c, attention._attn_call(
+        a["q"] or 0, a["qts"], a["qhs"], ctypes.addressof(c), a["table"] or 0, a["cols"], a["start"] or 0,
+        a["lens"] or 0, a["seqs"], a["tokens"], a["max_q"], a["max_len"], a["window"], a["out"] or 0, a["ots"],
+        a["ohs"], a["ws"] or 0, a["wsb"], 0, a["heads"], a["act"], a["sinks"], a["scale"])
+
+
+def _append_struct(cache=None, **kw):
+    a = dict(q=Q, qts=80 * 128, qhs=128, k=K, kts=80 * 128, khs=128, v=V, vts=80 * 128, vhs=128, qn=NORM, kn=None,
+             eps=1e-6, rope=ROPE, rows=4096, rot=128, inter=0, pos=POS, seq=None, table=TABLE, cols=64, seqs=4,
+             tokens=10, heads=64, act=F16, out=OUT, ots=64 * 128, ohs=128)
+    a.update(kw)
+    c = cache if cache is not None else _cache()
+    return c, attention._append_call(
+        a["q"] or 0, a["qts"], a["qhs"], a["k"] or 0, a["kts"], a["khs"], a["v"] or 0, a["vts"], a["vhs"],
+        a["qn"] or 0, a["kn"] or 0, a["rope"] or 0, a["rows"], a["pos"] or 0, a["seq"] or 0, a["table"] or 0,
+        a["cols"], a["seqs"], a["tokens"], ctypes.addressof(c), a["out"] or 0, a["ots"], a["ohs"], 0, a["rot"],
+        a["inter"], a["heads"], a["act"], a["eps"])
+
+
+# The calls by struct refuse what the calls by argument refuse: every field is where the library reads it.
+@pytest.mark.parametrize("fault,status", ATTN_FAULTS)
+def test_attention_faults_by_struct(fault, status):
+    c, call = _attn_struct(**fault)
+    for name in ("qgemm_attn_decode_call", "qgemm_attn_prefill_call"):
+        assert getattr(qg.lib(), name)(call) == status, name
+
+
+@pytest.mark.parametrize("fault,status", PREFILL_FAULTS)
+def test_prefill_faults_by_struct(fault, status):
+    c, call = _attn_struct(**fault)
+    assert qg.lib().qgemm_attn_prefill_call(call) == status
+
+
+def test_decode_by_struct_ignores_what_belongs_to_prefill():
+    c, call = _attn_struct(start=START + 2, tokens=-1, max_q=-1, seqs=0)
+    assert qg.lib().qgemm_attn_decode_call(call) == OK
+
+
+@pytest.mark.parametrize("fault,status", APPEND_FAULTS)
+def test_append_faults_by_struct(fault, status):
+    c, call = _append_struct(**fault)
+    assert qg.lib().qgemm_qk_rope_append_call(call) == status
+
+
+@pytest.mark.parametrize("fault,status", CACHE_FAULTS)
+def test_cache_faults_by_struct(fault, status):
+    c, call = _attn_struct(_cache(**fault))
+    assert qg.lib().qgemm_attn_decode_call(call) == status
+    assert qg.lib().qgemm_attn_prefill_call(call) == status
+    c, call = _append_struct(_cache(**fault))
+    assert qg.lib().qgemm_qk_rope_append_call(call) == status
+
+
+def test_null_structs():
+    for name in ("qgemm_attn_decode_call", "qgemm_attn_prefill_call", "qgemm_qk_rope_append_call"):
+        assert getattr(qg.lib(), name)(None) == NULL

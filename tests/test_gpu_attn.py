@@ -2,6 +2,7 @@
 fp64 oracle, each output within the bound derived from the number formats (oracle/attention.py). Memory that holds no
 token is NaN in every cache, and table entries past a sequence's end are out of range."""
 
+import ctypes
 import sys
 
 import numpy as np
@@ -529,3 +530,47 @@ def test_prefill_then_decode_equals_one_prefill():
         done += 1
     torch.cuda.synchronize()
     check(oa.decode(to_bits(torch.cat(rows)), act), refs, act, PREFILL_WEIGHTS[act], "chunks")
+
+
+def test_calls_by_argument_equal_the_binding():
+    _say("flat entry points")
+    rng = np.random.default_rng(33)
+    H, KV, D, act, lens, new = 8, 2, 64, "bf16", [70, 33], [5, 2]
+    pg = Paged(rng, lens, KV, D, act, 16, DEV)
+    L, scale = qg.lib(), 0.125
+    T = sum(new)
+    fused = to_torch(_values(rng, (T, H + 2 * KV, D), act)[0], act, DEV)
+    q, k, v = fused[:, :H], fused[:, H:H + KV], fused[:, H + KV:]
+    rope = qg.rope_table(80, D, device=DEV)
+    pos = torch.tensor([lens[0] - 5 + i for i in range(5)] + [31, 32], dtype=torch.int32, device=DEV)
+    seq = torch.tensor([0] * 5 + [1] * 2, dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, 5, 7], dtype=torch.int32, device=DEV)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    c, cols = pg.cache, pg.table_dev.shape[1]
+    ref = ctypes.byref(c._struct)
+    rotated = qg.qk_rope_append(q, k, v, pos, c, pg.table_dev, rope, token_seq=seq)
+    stored = c.k.clone(), c.v.clone()
+    out = torch.zeros_like(rotated)
+    assert L.qgemm_qk_rope_append(q.data_ptr(), q.stride(0), D, k.data_ptr(), k.stride(0), D, v.data_ptr(),
+                                  v.stride(0), D, None, None, 1e-6, rope.data_ptr(), 80, D, 0, pos.data_ptr(),
+                                  seq.data_ptr(), pg.table_dev.data_ptr(), cols, 2, T, H, qg.DT_BF16, ref,
+                                  out.data_ptr(), H * D, D, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, rotated)
+    for a, b in zip((c.k, c.v), stored):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device=DEV)
+    for splits in (1, 3):
+        qg.set_attn_splits(splits)
+        got = torch.zeros_like(rotated)
+        assert L.qgemm_attn_prefill(rotated.data_ptr(), H * D, D, ref, pg.table_dev.data_ptr(), cols, start.data_ptr(),
+                                    n.data_ptr(), 2, T, 5, 80, H, qg.DT_BF16, scale, 0, 0, got.data_ptr(), H * D, D,
+                                    ws.data_ptr(), ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(got, qg.attn_prefill(rotated, c, pg.table_dev, start, n, 5, 80, scale=scale))
+        got = torch.zeros_like(rotated[:2])
+        assert L.qgemm_attn_decode(rotated.data_ptr(), H * D, D, ref, pg.table_dev.data_ptr(), cols, n.data_ptr(), 2,
+                                   80, H, qg.DT_BF16, scale, 0, 0, got.data_ptr(), H * D, D, ws.data_ptr(), ws.numel(),
+                                   None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(got, qg.attn_decode(rotated[:2], c, pg.table_dev, n, 80, scale=scale))
