@@ -416,6 +416,14 @@ def test_prefill(new, lens, H, KV, D, act, cache, page, layout, window, sinks):
         check(oa.decode(to_bits(out), act), refs, act, _weights(PREFILL_WEIGHTS, act, cache), splits)
 
 
+# head sizes on both sides of every limit at which the products widen
+@pytest.mark.parametrize("D", [32, 80, 96, 112, 144, 160, 192, 208])
+@pytest.mark.parametrize("act,cache", [("f16", "f16"), ("bf16", "bf16"), ("bf16", "fp8")])
+def test_prefill_head_sizes(D, act, cache):
+    test_prefill([45, 70], [45, 333], 6, 2, D, act, cache, 16, "padded" if D % 32 else "heads", 0, 0)
+    test_prefill([70], [400], 3, 1, D, act, cache, 32, "tokens", 77, 5)
+
+
 def test_prefill_strided_rows_bounds_and_guards():
     _say("prefill strided and bounded")
     rng = np.random.default_rng(21)
