@@ -195,6 +195,25 @@ def test_append_e4m3_saturates_and_keeps_nan():
         assert np.array_equal(np.delete(got, 5), np.delete(want, 5))
 
 
+def test_append_offsets_beyond_32_bits():
+    _say("append far pages")
+    KV, D, page, pages, step = 2, 64, 16, 450, 10 << 20
+    k, v = (torch.zeros(pages * step, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    shape, stride = (pages, page, KV, D), (step, D, page * D, 1)
+    cache = qg.KVCache(k.as_strided(shape, stride), v.as_strided(shape, stride))
+    rng = np.random.default_rng(14)
+    fused = to_torch(_values(rng, (3, 3 * KV, D), "bf16")[0], "bf16", DEV)
+    table = torch.tensor([[449, 3, 420]], dtype=torch.int32, device=DEV)
+    pos = torch.tensor([5, 20, 47], dtype=torch.int32, device=DEV)
+    q = qg.qk_rope_append(fused[:, :KV], fused[:, KV:2 * KV], fused[:, 2 * KV:], pos, cache, table,
+                          token_seq=torch.zeros(3, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(q, fused[:, :KV])
+    for t, (pg, place) in enumerate([(449, 5), (3, 4), (420, 15)]):
+        assert torch.equal(cache.k[pg, place], fused[t, KV:2 * KV])
+        assert torch.equal(cache.v[pg, place], fused[t, 2 * KV:])
+
+
 def test_append_without_tokens():
     _say("append of nothing")
     pg = Paged(np.random.default_rng(6), [3], 2, 64, "f16", 16, DEV)
