@@ -13,7 +13,7 @@ import functools
 import math
 import struct
 
-from . import DT_BF16, DT_F16, DT_FP8, Workspace, _check, _default_ws, _raw_stream, _torch, lib
+from . import DT_BF16, DT_F16, DT_FP8, Workspace, _check, _default_ws, _torch, lib
 
 __all__ = ["KVCache", "rope_table", "qk_rope_append", "attn_decode", "attn_prefill", "set_attn_splits",
            "attn_decode_workspace_bytes", "attn_prefill_workspace_bytes"]
@@ -53,8 +53,12 @@ class KVCache:
             raise ValueError("a head's values must be contiguous")
         self.k, self.v, self.device = k, v, k.device
         self._index = k.get_device()   # the calls use this device's current stream
+        # what every call looks up, at hand: calls are bound by their host time when they move little
         torch = _torch()
         self._int32_type, self._float32_type = torch.int32, torch.float32
+        self._empty_like, self._stream = torch.empty_like, torch._C._cuda_getCurrentRawStream
+        self._acts = {torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+        self._norm_shape = torch.Size((k.shape[3],))
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.num_pages, k.stride(0), k.stride(1), k.stride(2),
@@ -118,8 +122,8 @@ def _queries(q, cache: KVCache, out):
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError(f"q must be [tokens][heads][head_dim of the cache], not {tuple(shape)}")
-    dt = _dtypes().get(q.dtype)
-    if dt is None or dt == DT_FP8:
+    dt = cache._acts.get(q.dtype)
+    if dt is None:
         raise ValueError("activations must be float16 or bfloat16")
     if q.get_device() != cache._index:
         raise ValueError("q must live on the cache's device")
@@ -127,12 +131,13 @@ def _queries(q, cache: KVCache, out):
     if one != 1:
         raise ValueError("q: a head's values must be contiguous")
     if out is None:
-        torch = _torch()
-        if hs == shape[2] and ts == shape[1] * hs:   # keeps such strides
-            out = torch.empty_like(q)
+        out_hs = shape[2]
+        out_ts = shape[1] * out_hs
+        if hs == out_hs and ts == out_ts:
+            out = cache._empty_like(q)   # keeps such strides
         else:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        oa = (out.data_ptr(), shape[1] * shape[2], shape[2])
+            out = cache._empty_like(q, memory_format=_torch().contiguous_format)
+        oa = (out.data_ptr(), out_ts, out_hs)
     else:
         oa = _heads(out, "out", shape, cache, q.dtype)
     return shape, dt, out, (q.data_ptr(), ts, hs), oa
@@ -141,7 +146,7 @@ def _queries(q, cache: KVCache, out):
 def _norm(w, name: str, cache: KVCache, dtype):
     if w is None:
         return 0
-    if w.dtype is not dtype or w.get_device() != cache._index or w.shape != (cache.head_dim,) or not w.is_contiguous():
+    if w.dtype is not dtype or w.get_device() != cache._index or w.shape != cache._norm_shape or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [head_dim] tensor of q's type")
     return w.data_ptr()
 
@@ -170,10 +175,12 @@ def qk_rope_append(q, k, v, positions, cache: KVCache, block_table, rope=None, q
             _norm(q_norm, "q_norm", cache, dtype), _norm(k_norm, "k_norm", cache, dtype), rope_at, rows,
             _int32(positions, "positions", cache, (T,)),
             0 if token_seq is None else _int32(token_seq, "token_seq", cache, (T,)), table, cols, seqs, T,
-            cache._address, *oa, _raw_stream(cache._index), rot, 1 if interleaved else 0, H, dt, eps)
+            cache._address, *oa, cache._stream(cache._index), rot, 1 if interleaved else 0, H, dt, eps)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"qk_rope_append: {e}") from None
-    _check(lib().qgemm_qk_rope_append_call(call), "qgemm_qk_rope_append")
+    status = lib().qgemm_qk_rope_append_call(call)
+    if status:
+        _check(status, "qgemm_qk_rope_append")
     return out
 
 
@@ -232,10 +239,12 @@ def attn_decode(q, cache: KVCache, block_table, seq_lens, max_len: int, scale: f
                          sinks)
     try:
         call = _attn_call(*qa, cache._address, table, cols, 0, lens, B, B, 1, max_len, window, *oa, ws, wsb,
-                          _raw_stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale)
+                          cache._stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"attn_decode: {e}") from None
-    _check(lib().qgemm_attn_decode_call(call), "qgemm_attn_decode")
+    status = lib().qgemm_attn_decode_call(call)
+    if status:
+        _check(status, "qgemm_attn_decode")
     return out
 
 
@@ -255,8 +264,10 @@ def attn_prefill(q, cache: KVCache, block_table, q_start, seq_lens, max_q: int, 
                          window, sinks)
     try:
         call = _attn_call(*qa, cache._address, table, cols, starts, lens, seqs, T, max_q, max_len, window, *oa, ws, wsb,
-                          _raw_stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale)
+                          cache._stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"attn_prefill: {e}") from None
-    _check(lib().qgemm_attn_prefill_call(call), "qgemm_attn_prefill")
+    status = lib().qgemm_attn_prefill_call(call)
+    if status:
+        _check(status, "qgemm_attn_prefill")
     return out
