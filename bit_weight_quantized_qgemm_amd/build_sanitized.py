@@ -14,6 +14,7 @@ Usage: ``python -m bit_weight_quantized_qgemm_amd.build_sanitized``.
 from __future__ import annotations
 
 import concurrent.futures
+import fcntl
 import os
 import subprocess
 import sys
@@ -48,6 +49,12 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    with open(os.path.join(BUILD, "lock"), "w") as lock:   # one build at a time: test processes share the objects
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        return _build(verbose)
+
+
+def _build(verbose: bool) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(_b.SOURCES))) as ex:
         objs = list(ex.map(_compile, _b.SOURCES))
     tmp = LIB + ".tmp"

@@ -109,11 +109,24 @@ int check_heads(int32_t q_heads, int32_t kv_heads) {
   return QGEMM_OK;
 }
 
+// What the callers' window and sinks mean for contexts of up to max_len tokens: a
+// window beyond every position is none (0, and then there are no sinks), sinks beyond
+// the context are all of it. Plans and kernels take these alone, so that both see the
+// same tokens and sums over them stay small whatever the caller passed.
+struct Mask {
+  int64_t window, sinks;
+};
+Mask bounded_mask(int64_t max_len, int64_t window, int64_t sinks) {
+  if (window >= max_len) return Mask{0, 0};
+  return Mask{window, window == 0 ? 0 : std::min(sinks, max_len)};
+}
+
 // Most token blocks that a sequence has to visit.
-int64_t visible_blocks(int64_t max_len, int64_t rows, int64_t window, int32_t sinks) {
+int64_t visible_blocks(int64_t max_len, int64_t rows, const Mask& mask) {
   const int64_t all = (max_len + qg::kTokBlock - 1) / qg::kTokBlock;
-  if (window == 0) return all;
-  return std::min(all, (sinks + qg::kTokBlock - 1) / qg::kTokBlock + (window + rows - 1 + 2 * qg::kTokBlock - 2) / qg::kTokBlock);
+  if (mask.window == 0) return all;
+  return std::min(all, (mask.sinks + qg::kTokBlock - 1) / qg::kTokBlock +
+                           (mask.window + rows - 1 + 2 * qg::kTokBlock - 2) / qg::kTokBlock);
 }
 
 void split(qg::AttnPlan& pl, int64_t blocks, int64_t want, int step, int head_dim) {
@@ -134,14 +147,14 @@ void split(qg::AttnPlan& pl, int64_t blocks, int64_t want, int step, int head_di
   }
 }
 
-qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_heads, int head_dim, int64_t window,
-                         int32_t sinks) {
+qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_heads, int head_dim,
+                         const Mask& mask) {
   qg::AttnPlan pl;
   const int group = q_heads / kv_heads;
   pl.row_tiles = (group + qg::kDecodeRows - 1) / qg::kDecodeRows;
   pl.part_rows = std::min(group, qg::kDecodeRows);
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
-  const int64_t blocks = visible_blocks(max_len, 1, window, sinks);
+  const int64_t blocks = visible_blocks(max_len, 1, mask);
   constexpr int kStep = 2 * qg::kDecodeWaves;   // one pair of blocks for each wave
   const int64_t steps = (blocks + kStep - 1) / kStep;
   // Parts of a tile, by tiles per compute unit and steps (128 tokens) of the longest
@@ -177,13 +190,13 @@ qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_
 }
 
 qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int q_heads, int kv_heads, int head_dim,
-                          int64_t window, int32_t sinks) {
+                          const Mask& mask) {
   qg::AttnPlan pl;
   const int64_t rows = max_q * (q_heads / kv_heads);
   pl.row_tiles = (int)((rows + qg::kPrefillRows - 1) / qg::kPrefillRows);
   pl.part_rows = (int)std::min<int64_t>(rows, qg::kPrefillRows);
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
-  const int64_t blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), window, sinks);
+  const int64_t blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), mask);
   // Tiles of K and V hold 64 tokens (32 for heads above 128 values). One takes a
   // workgroup that has a compute unit for itself 1.25 us, and w of them that share a
   // unit 1.15 w us together (0.9 and 0.65 w for heads of 64); a join of s parts, x MB,
@@ -203,7 +216,7 @@ qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int 
     const int steps = (int)((blocks + kStep - 1) / kStep), tiles = (int)pl.tiles;
     const double part_mb = (double)tiles * pl.part_rows * head_dim * 4e-6;
     const double alone = head_dim <= 64 ? 0.9 : 1.25, shared = head_dim <= 64 ? 0.65 : 1.15;
-    const bool even = window != 0 || max_q * 5 < max_len;
+    const bool even = mask.window != 0 || max_q * 5 < max_len;
     const double mean = even ? 1 : 1 - 0.5 * std::min(max_q, max_len) / (double)max_len;   // of a tile's visible part
     double least = 0;
     for (int s = 1; s <= steps && s * tiles <= 8 * cus && s <= 2 * cus; s += s < 32 ? 1 : 16) {
@@ -255,9 +268,10 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
   if (g.table_stride < 0 || g.table_stride > kMaxLen || g.max_len > g.table_stride * c->page_size)
     return QGEMM_ERR_SHAPE;
 
-  const qg::AttnPlan pl =
-      prefill ? prefill_plan(g.num_seqs, max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks)
-              : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
+  const Mask mask = bounded_mask(g.max_len, g.window, g.sinks);
+  const qg::AttnPlan pl = prefill
+                              ? prefill_plan(g.num_seqs, max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask)
+                              : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask);
   if (pl.tiles * pl.splits > INT32_MAX) return QGEMM_ERR_SHAPE;
   if (pl.ws_bytes > 0) {
     if (!g.workspace) return QGEMM_ERR_NULL;
@@ -297,9 +311,8 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
   a.num_tokens = (int32_t)num_tokens;
   a.max_q = (int32_t)max_q;
   a.max_len = (int32_t)g.max_len;
-  // a window beyond every position is none; sinks beyond max_len are all tokens
-  a.window = g.window >= g.max_len ? 0 : (int32_t)g.window;
-  a.sinks = (int32_t)std::min<int64_t>(g.sinks, g.max_len);
+  a.window = (int32_t)mask.window;
+  a.sinks = (int32_t)mask.sinks;
   a.row_tiles = pl.row_tiles;
   a.part_rows = pl.part_rows;
   a.splits = pl.splits;
@@ -465,7 +478,8 @@ int qgemm_attn_decode_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t
   if (!bytes) return QGEMM_ERR_NULL;
   const int st = check_attn_shape(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks);
   if (st) return st;
-  *bytes = num_seqs == 0 ? 0 : decode_plan(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks).ws_bytes;
+  const Mask mask = bounded_mask(max_len, window, sinks);
+  *bytes = num_seqs == 0 ? 0 : decode_plan(num_seqs, max_len, q_heads, kv_heads, head_dim, mask).ws_bytes;
   return QGEMM_OK;
 }
 
@@ -509,9 +523,10 @@ int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t 
   const int st = check_attn_shape(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks);
   if (st) return st;
   if (max_q < 0 || max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
+  const Mask mask = bounded_mask(max_len, window, sinks);
   *bytes = num_seqs == 0 || max_q == 0
                ? 0
-               : prefill_plan(num_seqs, max_q, max_len, q_heads, kv_heads, head_dim, window, sinks).ws_bytes;
+               : prefill_plan(num_seqs, max_q, max_len, q_heads, kv_heads, head_dim, mask).ws_bytes;
   return QGEMM_OK;
 }
 

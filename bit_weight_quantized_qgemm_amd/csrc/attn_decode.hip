@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
 
   const int len = min(max(scalar_load(p.lens + seq), 0), p.max_len);
   const Visible see(len, p.window ? len - p.window : 0, p.window ? p.sinks : 0);
-  const int parts = max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks);
+  // never more than the workspace holds (the plan covers see.blocks with p.splits)
+  const int parts = p.splits == 1 ? 1 : min(p.splits, max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks));
   if (split >= parts) return;
   const int v_end = min(see.blocks, (split + 1) * p.split_blocks);
 

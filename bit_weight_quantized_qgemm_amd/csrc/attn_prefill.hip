@@ -141,7 +141,7 @@ __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& p, int tile) {
   const int pos_min = pos0 + divide_uniform(row0, p.inv_group);
   const int pos_max = pos0 + divide_uniform(row0 + max(1, rows) - 1, p.inv_group);
   const Visible see(max(0, pos_max + 1), p.window ? pos_min - p.window + 1 : 0, p.window ? p.sinks : 0);
-  const int parts = p.splits == 1 ? 1 : max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks);
+  const int parts = p.splits == 1 ? 1 : min(p.splits, max(1, (see.blocks + p.split_blocks - 1) / p.split_blocks));
   return RowTile{seq, kv_head, row0, rows, all_rows, q0, pos0, pos_min, pos_max, see, parts};
 }
 

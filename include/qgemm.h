@@ -390,7 +390,8 @@ int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
  * (j < n, n = seq_lens[b], the new token's own included):
  *   out[b,h] = sum_j softmax_j(scale * q[b,h] . k[j]) v[j]
  * window = 0: every j < n is visible; window > 0: the last `window` tokens and
- * the first `sinks` ones (j >= n - window or j < sinks) are. Masked keys and
+ * the first `sinks` ones (j >= n - window or j < sinks) are. Neither has an upper
+ * limit: from max_len on they show every token. Masked keys and
  * values are never used, whatever their memory holds. A sequence without visible
  * tokens (n <= 0, or no page in range) gives zeros. seq_lens is int32
  * [num_seqs] in device memory; lengths above max_len are taken as max_len.
