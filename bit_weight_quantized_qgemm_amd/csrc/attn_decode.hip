@@ -24,8 +24,9 @@
 //   P    the scores leave the matrix unit with head c and tokens 4h..4h+3 of
 //        each block in lane (c, h): with the tokens of V in that order they are
 //        the second operand as they stand. Weights go in as two 16-bit terms (the
-//        rounded weight and the rest), so rounding them costs no accuracy; the
-//        matrix unit has the time.
+//        rounded weight and the rest), good to 2^-22 (fp16) or 2^-16 (bf16) of each
+//        and, in fp16, no finer than 2^-36 of the largest; the matrix unit has the
+//        time.
 // K of the next pair is requested as soon as this pair's scores are done and V
 // once its outputs are, so one of the two is always on its way. Tokens past the
 // end, pages out of range and dimensions past head_dim are cut off by the size
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
     float top = t[0];
 #pragma unroll
     for (int r = 1; r < 8; ++r) top = fmaxf(top, t[r]);
-    if (__any(top > mref + kSlack)) {
+    if (__any(top > mref + PF::kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = fmaxf(mref, top);
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[j][i][r] *= f;
     }
-    const float base = mref == kNegInf ? 0.f : mref;
+    const float base = weight_base<PF>(mref);
     u32x4 w, wl;   // the weights in 16 bits, and what that leaves
 #pragma unroll
     for (int r = 0; r < 8; ++r) {

@@ -397,7 +397,9 @@ int qgemm_qk_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
  * [num_seqs] in device memory; lengths above max_len are taken as max_len.
  * Scores, softmax statistics and sums are fp32; each softmax weight goes to the
  * matrix cores as two 16-bit terms (fp16, or bfloat16 against a bfloat16 cache),
- * each output is rounded once to act_dtype. scale must be finite and > 0.
+ * each output is rounded once to act_dtype. In fp16 a weight is held no finer than
+ * 2^-36 of its row's largest; tokens further below (25 nats) count as absent.
+ * scale must be finite and > 0.
  *
  * The cache's length is split over workgroups when there are few rows; the last
  * workgroup of a row joins the parts in order, so results do not change from run
