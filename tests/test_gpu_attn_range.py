@@ -1,5 +1,6 @@
 """GPU parity of the attention operators at the ends of what their arguments may be, against the fp64 oracle as in
-tests/test_gpu_attn.py: masks beyond the context, weights far below the largest."""
+tests/test_gpu_attn.py: masks beyond the context, weights far below the
+largest, contexts of several groups of pages and parts."""
 
 import numpy as np
 import pytest
@@ -88,3 +89,78 @@ def test_a_first_token_far_above_the_rest(act, cache):
             off = (np.abs(got - ref) / bound).max(axis=1)
             print([f"{x:.3f}" for x in off], flush=True)
             assert np.all(off <= 1), (splits, off)
+
+
+# A part of the prefill kernel looks its pages up for 64 blocks (1024 tokens) at a time: contexts of two and three such
+# groups, windows that begin inside one, and pages lost on both sides of each change.
+# heads, kv heads, dim, act, cache, page, layout, window, sinks
+GROUPS = [
+    (4, 2, 128, "f16", "f16", 16, "heads", 0, 0), (2, 1, 64, "bf16", "bf16", 16, "padded", 0, 0),
+    (2, 1, 256, "f16", "f16", 32, "heads", 0, 0), (2, 2, 192, "bf16", "bf16", 16, "tokens", 0, 0),
+    (2, 1, 96, "f16", "f16", 16, "heads", 0, 0), (4, 2, 128, "bf16", "fp8", 16, "tokens", 0, 0),
+    (2, 1, 64, "f16", "fp8", 16, "heads", 0, 0), (2, 1, 256, "bf16", "fp8", 16, "heads", 0, 0),
+    (4, 2, 128, "bf16", "bf16", 16, "heads", 1500, 37), (2, 1, 256, "f16", "f16", 16, "heads", 1111, 5),
+    (2, 1, 128, "f16", "fp8", 16, "padded", 1300, 200),
+]
+
+
+@pytest.mark.parametrize("lost", [False, True], ids=["whole", "lost pages"])
+@pytest.mark.parametrize("H,KV,D,act,cache,page,layout,window,sinks", GROUPS)
+def test_contexts_of_several_page_groups(H, KV, D, act, cache, page, layout, window, sinks, lost):
+    _say("page groups", H, KV, D, act, cache, page, layout, window, sinks, lost)
+    rng = np.random.default_rng(42 + D)
+    lens, new = [1100, 2300, 1024, 3200], [40, 5, 33, 2]
+    at = [1024 // page - 1, 1024 // page]   # the pages before and after the change
+    missing = [(0, at[0], 0), (1, at[0], -7), (1, at[1], 3), (1, 2 * at[1], 0), (3, 2 * at[1] - 1, -1), (3, 3 * at[1], 5)]
+    pg = Paged(rng, lens, KV, D, cache, page, DEV, layout, (0.25, 0.125) if cache == "fp8" else (1.0, 1.0),
+               missing=missing if lost else ())
+    bits, q = _values(rng, (sum(new), H, D), act, 2.0)
+    qd = to_torch(bits, act, DEV)
+    scale = np.float32(D ** -0.5).astype(np.float64)
+    kind = "f16" if cache == "fp8" else act
+    refs = _prefill_refs(pg, q, new, scale, window, sinks)
+    one = _decode_refs(pg, q, scale, window, sinks)
+    for splits in (0, 1, 2):
+        qg.set_attn_splits(splits)
+        out = _prefill(pg, qd, new, window=window, sinks=sinks)
+        last = _decode(pg, qd[:4], window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        check(oa.decode(to_bits(out), act), refs, act, PREFILL_WEIGHTS[kind], ("prefill", splits))
+        check(oa.decode(to_bits(last), act), one, act, DECODE_WEIGHTS[kind], ("decode", splits))
+
+
+def _set_key(pg, b, j, head, x):
+    """Token j of sequence b gets the key x (values) in one head."""
+    bits = oa.encode(np.asarray(x) / pg.scales[0], pg.fmt)
+    pg.k[int(pg.table[b, j // pg.page]), j % pg.page, head] = to_torch(bits, pg.fmt, DEV)
+    pg.tokens[b][0][j, head] = oa.decode(bits, pg.fmt) * pg.scales[0]
+
+
+# Joins read 16 parts at a time: parts in the second and third such batch, of which some sequences have none, and
+# scores that pass all earlier ones there (or in the first part).
+@pytest.mark.parametrize("peaks", [(4400, 2250, 650, 10), (3, 100, 680, 0)], ids=["late", "early"])
+@pytest.mark.parametrize("H,KV,D,act,cache", [(4, 2, 128, "f16", "f16"), (3, 1, 256, "bf16", "bf16"),
+                                              (2, 1, 64, "bf16", "bf16"), (4, 1, 80, "bf16", "fp8")])
+def test_joins_of_many_parts(H, KV, D, act, cache, peaks):
+    _say("many parts", H, KV, D, act, cache, peaks)
+    rng = np.random.default_rng(43 + D)
+    lens, new = [4500, 2300, 700, 20], [3, 9, 40, 2]
+    pg = Paged(rng, lens, KV, D, cache, 16, DEV, "heads", (0.25, 0.125) if cache == "fp8" else (1.0, 1.0))
+    bits, q = _values(rng, (sum(new), H, D), act)
+    qd = to_torch(bits, act, DEV)
+    scale = np.float32(D ** -0.5).astype(np.float64)
+    kind = "f16" if cache == "fp8" else act
+    ends = np.cumsum(new)
+    for b, j in enumerate(peaks):
+        # about 1.5 sqrt(D) nats for the last row's first head, and the same for the decoded row's
+        _set_key(pg, b, j, 0, 1.5 * q[ends[b] - 1, 0])
+        _set_key(pg, b, j + 1, KV - 1, 1.5 * q[b, H - 1])
+    refs, one = _prefill_refs(pg, q, new, scale), _decode_refs(pg, q, scale)
+    for splits in (17, 40, 1024):
+        qg.set_attn_splits(splits)
+        out, again = (_prefill(pg, qd, new) for _ in range(2))
+        last, once_more = (_decode(pg, qd[:4]) for _ in range(2))
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and torch.equal(last, once_more)
+        check(oa.decode(to_bits(out), act), refs, act, PREFILL_WEIGHTS[kind], ("prefill", splits))
+        check(oa.decode(to_bits(last), act), one, act, DECODE_WEIGHTS[kind], ("decode", splits))
