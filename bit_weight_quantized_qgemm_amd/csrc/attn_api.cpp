@@ -19,7 +19,6 @@ constexpr int64_t kMaxTokens = int64_t(1) << 20;
 constexpr int64_t kMaxLen = int64_t(1) << 24;
 constexpr int kMaxKvHeads = 1024;
 constexpr int kMaxGroup = 128;
-constexpr int kMaxHeadDim = 256;
 constexpr int64_t kMaxTokenStride = int64_t(1) << 25;
 
 std::atomic<int> g_force_splits{0};
@@ -61,7 +60,7 @@ bool valid_out_strides(int64_t tokens, int64_t ts, int64_t hs, int64_t heads, in
 
 int check_cache(const qgemm_kv_cache* c, int act_dtype) {
   if (c->kv_heads < 1 || c->kv_heads > kMaxKvHeads) return QGEMM_ERR_SHAPE;
-  if (c->head_dim < 16 || c->head_dim > kMaxHeadDim || c->head_dim % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (c->head_dim < 16 || c->head_dim > qg::kMaxHeadDim || c->head_dim % 16 != 0) return QGEMM_ERR_SHAPE;
   if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16 != 0) return QGEMM_ERR_SHAPE;
   if (c->num_pages < 1 || c->num_pages > INT32_MAX) return QGEMM_ERR_SHAPE;
   if (c->dtype != QGEMM_DT_F16 && c->dtype != QGEMM_DT_BF16 && c->dtype != QGEMM_DT_FP8) return QGEMM_ERR_RANGE;
@@ -239,7 +238,7 @@ int check_attn_shape(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t
   if (num_seqs < 0 || num_seqs > kMaxSeqs) return QGEMM_ERR_SHAPE;
   if (max_len < 0 || max_len > kMaxLen) return QGEMM_ERR_SHAPE;
   if (kv_heads < 1 || kv_heads > kMaxKvHeads) return QGEMM_ERR_SHAPE;
-  if (head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0) return QGEMM_ERR_SHAPE;
+  if (head_dim < 16 || head_dim > qg::kMaxHeadDim || head_dim % 16 != 0) return QGEMM_ERR_SHAPE;
   if (window < 0 || sinks < 0) return QGEMM_ERR_RANGE;
   return check_heads(q_heads, kv_heads);
 }

@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
   // part number in equal shares
   const int heads = p.kv_heads * p.row_tiles;
   const int tiles = p.num_seqs * heads;
-  const int split = p.splits == 1 ? 0 : divide_uniform(blockIdx.x, p.inv_tiles), tile = blockIdx.x - split * tiles;
+  const int block = blockIdx.x + p.first_block;
+  const int split = p.splits == 1 ? 0 : divide_uniform(block, p.inv_tiles), tile = block - split * tiles;
   const int seq = divide_uniform(tile, p.inv_heads);
   const int row_tile = p.row_tiles == 1 ? 0 : (tile - seq * heads) % p.row_tiles;
   const int kv_head = p.row_tiles == 1 ? tile - seq * heads : (tile - seq * heads) / p.row_tiles;
@@ -373,10 +374,12 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
 
 template <class F, class PF, bool FP8, int DP>
 hipError_t launch_exact(const AttnArgs& a, int64_t tiles, hipStream_t s) {
-  const dim3 grid((unsigned)(tiles * a.splits));
-  if (a.head_dim == DP) hipLaunchKernelGGL((attn_decode<F, PF, FP8, DP, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attn_decode<F, PF, FP8, DP, false>), grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  return launch_in_runs(tiles * a.splits, [&](dim3 grid, uint32_t first) {
+    AttnArgs r = a;
+    r.first_block = first;
+    if (a.head_dim == DP) hipLaunchKernelGGL((attn_decode<F, PF, FP8, DP, true>), grid, dim3(256), 0, s, r);
+    else hipLaunchKernelGGL((attn_decode<F, PF, FP8, DP, false>), grid, dim3(256), 0, s, r);
+  });
 }
 
 template <class F, class PF, bool FP8>

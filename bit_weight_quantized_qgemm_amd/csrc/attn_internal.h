@@ -17,7 +17,20 @@ constexpr int kTokBlock = 16;
 constexpr int kDecodeWaves = 4;
 constexpr int kDecodeRows = 16;       // query heads of one workgroup (MFMA columns)
 constexpr int kPrefillRows = 128;     // rows (heads of tokens) of one workgroup
+constexpr int kMaxHeadDim = 256;
 constexpr int kMaxAttnSplits = 1024;
+// A launch has fewer than 2^32 threads: grids of 256-thread workgroups above this many
+// go out as several launches, each telling its first workgroup's number.
+constexpr int64_t kMaxGrid = int64_t(1) << 23;
+template <class Launch>
+hipError_t launch_in_runs(int64_t workgroups, const Launch& launch) {
+  for (int64_t first = 0; first < workgroups; first += kMaxGrid) {
+    launch(dim3((unsigned)(workgroups - first < kMaxGrid ? workgroups - first : kMaxGrid)), (uint32_t)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 // The cache as the kernels see it. `magic` divides a block number (below 2^20)
 // by page_blocks (at most 2^12): n / d = (n * magic) >> 32 with
@@ -54,6 +67,7 @@ struct AttnArgs {
   double inv_group, inv_kv_heads, inv_seqs, inv_heads, inv_tiles;   // 1 / group, ... (heads: row tiles of a sequence)
   float scale_log2;         // scale * k_scale * log2(e)
   float v_scale;
+  uint32_t first_block;     // number of the launch's first workgroup
 };
 
 struct AttnPlan {
@@ -83,6 +97,7 @@ struct AppendArgs {
   int32_t num_seqs, num_tokens, q_heads, kv_heads, head_dim;
   void* q_out;
   float k_scale, v_scale;
+  uint32_t first_block;   // number of the launch's first workgroup
 };
 
 hipError_t launch_append(const AppendArgs& a, bool bf16, bool fp8, bool interleaved, hipStream_t s);

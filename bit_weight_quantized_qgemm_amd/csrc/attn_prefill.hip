@@ -166,7 +166,8 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = p.num_seqs * p.kv_heads * p.row_tiles;
-  const int split = p.splits == 1 ? 0 : divide_uniform(blockIdx.x, p.inv_tiles), tile = blockIdx.x - split * tiles;
+  const int block = blockIdx.x + p.first_block;
+  const int split = p.splits == 1 ? 0 : divide_uniform(block, p.inv_tiles), tile = block - split * tiles;
   const RowTile rt = row_tile_of(p, tile);
   if (rt.rows <= 0 || split >= rt.parts) return;
   const Visible& see = rt.see;
@@ -629,14 +630,18 @@ __global__ void __launch_bounds__(256) attn_prefill_join(AttnArgs p, int chunks)
 
 template <class F, class PF, bool FP8, int DP, int DU>
 hipError_t launch_exact(const AttnArgs& a, int64_t tiles, hipStream_t s) {
-  const dim3 grid((unsigned)(tiles * a.splits));
   constexpr int lds = PrefillLds<DP>::kTotal;
-  if (DU == DP && a.head_dim == DP)
-    hipLaunchKernelGGL((attn_prefill<F, PF, FP8, DP, DP, true>), grid, dim3(256), lds, s, a);
-  else
-    hipLaunchKernelGGL((attn_prefill<F, PF, FP8, DP, DU, false>), grid, dim3(256), lds, s, a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = launch_in_runs(tiles * a.splits, [&](dim3 grid, uint32_t first) {
+    AttnArgs r = a;
+    r.first_block = first;
+    if (DU == DP && a.head_dim == DP)
+      hipLaunchKernelGGL((attn_prefill<F, PF, FP8, DP, DP, true>), grid, dim3(256), lds, s, r);
+    else
+      hipLaunchKernelGGL((attn_prefill<F, PF, FP8, DP, DU, false>), grid, dim3(256), lds, s, r);
+  });
   if (e != hipSuccess || a.splits == 1) return e;
+  // at most kMaxCounters tiles are split, in 32 chunks each: one launch
+  static_assert(kMaxCounters * (kPrefillRows * kMaxHeadDim / 4 / 256) <= kMaxGrid, "the join's grid");
   const int chunks = (a.part_rows * (a.head_dim / 4) + 255) / 256;
   hipLaunchKernelGGL((attn_prefill_join<F>), dim3((unsigned)(tiles * chunks)), dim3(256), 0, s, a, chunks);
   return hipGetLastError();

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) rope_append(AppendArgs p) {
   const int lane = threadIdx.x % LANES;
   const int heads = p.q_heads + 2 * p.kv_heads;
   // below 2^31, or in the last workgroup a little above, which wraps to a negative
-  const int task = (int)(blockIdx.x * (uint32_t)kHeads + threadIdx.x / LANES);
+  const int task = (int)((blockIdx.x + p.first_block) * (uint32_t)kHeads + threadIdx.x / LANES);
   const int token = divide(task, p.inv_heads);
   if (task < 0 || token >= p.num_tokens) return;   // whole heads of lanes leave together
   int head = task - token * heads;
@@ -169,13 +169,15 @@ template <class F, bool FP8, bool INTERLEAVED>
 hipError_t launch_lanes(const AppendArgs& a, hipStream_t s) {
   const int lanes = a.head_dim <= 64 ? 4 : a.head_dim <= 128 ? 8 : 16;
   const int64_t tasks = (int64_t)a.num_tokens * (a.q_heads + 2 * a.kv_heads);
-  const dim3 grid((unsigned)((tasks * lanes + 255) / 256));
-  switch (lanes) {
-    case 4: hipLaunchKernelGGL((rope_append<F, FP8, INTERLEAVED, 4>), grid, dim3(256), 0, s, a); break;
-    case 8: hipLaunchKernelGGL((rope_append<F, FP8, INTERLEAVED, 8>), grid, dim3(256), 0, s, a); break;
-    default: hipLaunchKernelGGL((rope_append<F, FP8, INTERLEAVED, 16>), grid, dim3(256), 0, s, a); break;
-  }
-  return hipGetLastError();
+  return launch_in_runs((tasks * lanes + 255) / 256, [&](dim3 grid, uint32_t first) {
+    AppendArgs r = a;
+    r.first_block = first;
+    switch (lanes) {
+      case 4: hipLaunchKernelGGL((rope_append<F, FP8, INTERLEAVED, 4>), grid, dim3(256), 0, s, r); break;
+      case 8: hipLaunchKernelGGL((rope_append<F, FP8, INTERLEAVED, 8>), grid, dim3(256), 0, s, r); break;
+      default: hipLaunchKernelGGL((rope_append<F, FP8, INTERLEAVED, 16>), grid, dim3(256), 0, s, r); break;
+    }
+  });
 }
 
 template <class F>

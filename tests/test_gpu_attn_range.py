@@ -1,6 +1,7 @@
 """GPU parity of the attention operators at the ends of what their arguments may be, against the fp64 oracle as in
 tests/test_gpu_attn.py: masks beyond the context, weights far below the
-largest, contexts of several groups of pages and parts."""
+largest, contexts of several groups of pages and parts, calls of more workgroups than one launch
+holds."""
 
 import numpy as np
 import pytest
@@ -164,3 +165,83 @@ def test_joins_of_many_parts(H, KV, D, act, cache, peaks):
         assert torch.equal(out, again) and torch.equal(last, once_more)
         check(oa.decode(to_bits(out), act), refs, act, PREFILL_WEIGHTS[kind], ("prefill", splits))
         check(oa.decode(to_bits(last), act), one, act, DECODE_WEIGHTS[kind], ("decode", splits))
+
+
+# -------------------------------------------------------------- more workgroups than one launch holds (2^24 and above)
+def _pages(rng, pages, KV, D):
+    kv = [to_torch(_values(rng, (pages, 16, KV, D), "f16")[0], "f16", DEV) for _ in range(2)]
+    return qg.KVCache(*kv)
+
+
+def test_prefill_of_many_row_tiles():
+    _say("prefill of 2^24 row tiles")
+    rng = np.random.default_rng(44)
+    # 1024 sequences, 128 heads to one key-value head: up to 16384 new tokens are 16384 row tiles of each sequence
+    B, H, D, most, pages = 1024, 128, 16, 16384, 1100
+    cache = _pages(rng, pages, 1, D)
+    lens = rng.integers(1, 60, B)
+    long = 700
+    lens[long] = most
+    new = np.minimum(lens, rng.integers(1, 4, B))
+    new[long] = most
+    table = torch.from_numpy(rng.integers(0, pages, (B, most // 16)).astype(np.int32)).to(DEV)
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=DEV)
+    lens = torch.from_numpy(lens.astype(np.int32)).to(DEV)
+    T, at = int(new.sum()), int(new[:long].sum())
+    q = torch.randn((T, H, D), dtype=torch.float32, device=DEV).to(torch.float16)
+    out = torch.full_like(q, float("nan"))
+    qg.set_attn_splits(1)
+    qg.attn_prefill(q, cache, table, starts, lens, most, most, out=out)
+    # the same sequences in two calls of few row tiles: the long one, and the others
+    alone = qg.attn_prefill(q[at:at + most], cache, table[long:long + 1], starts[:2] * 0 + torch.tensor(
+        [0, most], dtype=torch.int32, device=DEV), lens[long:long + 1], most, most)
+    rest = torch.full_like(q, float("nan"))
+    qg.attn_prefill(q, cache, table, starts, lens, 3, most, out=rest)
+    torch.cuda.synchronize()
+    assert not bool(out.isnan().any())
+    assert torch.equal(out[at:at + most], alone)
+    rest[at:at + most] = alone
+    assert torch.equal(out, rest)
+
+
+def test_decode_of_many_tiles():
+    _say("decode of 65535 x 256 tiles")
+    rng = np.random.default_rng(45)
+    B, H, D, pages = 65535, 256, 16, 40
+    cache = _pages(rng, pages, H, D)
+    table = torch.from_numpy(rng.integers(0, pages, (B, 2)).astype(np.int32)).to(DEV)
+    lens = torch.from_numpy(rng.integers(0, 33, B).astype(np.int32)).to(DEV)
+    q = torch.randn((B, H, D), dtype=torch.float32, device=DEV).to(torch.float16)
+    out = qg.attn_decode(q, cache, table, lens, 32, out=torch.full_like(q, float("nan")))
+    torch.cuda.synchronize()
+    for a in range(0, B, 16384):   # calls of one launch each
+        e = min(B, a + 16384)
+        assert torch.equal(out[a:e], qg.attn_decode(q[a:e], cache, table[a:e], lens[a:e], 32)), a
+
+
+def test_append_of_many_heads():
+    _say("append of 2^20 x 1026 heads")
+    T, H, D = 1 << 20, 342, 16
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(46)
+    q = torch.empty((T, H, D), dtype=torch.float16, device=DEV).normal_(generator=gen)
+    k, v = (torch.randn((1, H, D), generator=gen, device=DEV).to(torch.float16).expand(T, H, D) for _ in range(2))
+    cache = qg.KVCache.empty(2, 16, H, D, torch.float16, DEV)
+    table = torch.tensor([[-1], [1]], dtype=torch.int32, device=DEV)
+    pos = torch.zeros(T, dtype=torch.int32, device=DEV)
+    seq = torch.zeros(T, dtype=torch.int32, device=DEV)   # whose page is out of range: rotated, not stored
+    kept = {0: 3, T // 2 + 1: 7, T - 1: 12}
+    for t, p in kept.items():
+        seq[t], pos[t] = 1, p
+    pos[5] = -1
+    out = torch.full_like(q, float("nan"))
+    qg.qk_rope_append(q, k, v, pos, cache, table, token_seq=seq, out=out)
+    torch.cuda.synchronize()
+    q[5] = 0
+    assert all(torch.equal(out[a:a + (T >> 4)], q[a:a + (T >> 4)]) for a in range(0, T, T >> 4))
+    del q, out
+    torch.cuda.empty_cache()
+    for buf, new in ((cache.k, k), (cache.v, v)):
+        assert not bool(buf[0].any())
+        for p in range(16):
+            assert torch.equal(buf[1, p], new[0] if p in kept.values() else torch.zeros_like(new[0])), p
