@@ -229,13 +229,19 @@ class Workspace:
 
     The kernels leave the counter region zero after each completed call, so the
     buffer is cleared only when it is (re)allocated. Calls that share one
-    workspace buffer must run in order, so each stream gets its own buffer
-    (allocated while that stream is current: the caching allocator then reuses
-    a grown-out buffer's memory only in that stream's order).
+    workspace buffer must run in order, so each stream gets its own buffer.
+
+    Graphs: a captured call keeps the address that it was given, so a buffer that
+    was grown out of stays allocated as long as the workspace (each is at least
+    twice the one before, which bounds what they hold together). A call that finds
+    no buffer large enough while its stream captures gets one of its own, which the
+    graph clears at each replay and no other call uses; running the call once on
+    that stream before the capture saves that.
     """
 
     def __init__(self):
         self._bufs = {}
+        self._outgrown = []
 
     def get(self, nbytes: int, device):
         if nbytes == 0:
@@ -247,7 +253,13 @@ class Workspace:
         key = (idx, _raw_stream(idx))
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
-            buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            if torch.cuda.is_current_stream_capturing():
+                return torch.zeros(nbytes, dtype=torch.uint8, device=device), nbytes
+            size = max(nbytes, 1 << 20)
+            if buf is not None:
+                size = max(size, 2 * buf.numel())
+                self._outgrown.append(buf)
+            buf = torch.zeros(size, dtype=torch.uint8, device=device)
             self._bufs[key] = buf
         return buf, buf.numel()
 
