@@ -46,15 +46,19 @@ Extent extent3(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t
   return extent(p, (tokens - 1) * ts + (heads - 1) * hs + dim, 2);
 }
 
+// A stride that n places are apart by: not used where there is one.
+bool valid_step(int64_t n, int64_t stride, int64_t multiple, int64_t most) {
+  return n == 1 || (stride >= 0 && stride <= most && stride % multiple == 0);
+}
 // Strides of a [tokens][heads][dim] tensor: 16-byte rows that do not overlap
 // within a token; bounded so that no extent overflows.
-bool valid_strides(int64_t ts, int64_t hs, int64_t heads, int64_t dim) {
+bool valid_strides(int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t dim) {
   constexpr int64_t kMost = int64_t(1) << 32;
-  return ts >= 0 && hs >= 0 && ts <= kMost && hs <= kMost && ts % 8 == 0 && hs % 8 == 0 && (heads == 1 || hs >= dim);
+  return valid_step(tokens, ts, 8, kMost) && valid_step(heads, hs, 8, kMost) && (heads == 1 || hs >= dim);
 }
 // ... of one that is written: its tokens must not overlap either.
-bool valid_out_strides(int64_t tokens, int64_t ts, int64_t hs, int64_t heads, int64_t dim) {
-  return valid_strides(ts, hs, heads, dim) &&
+bool valid_out_strides(int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t dim) {
+  return valid_strides(tokens, ts, heads, hs, dim) &&
          (tokens == 1 || ts >= (heads - 1) * hs + dim || (ts >= dim && hs >= (tokens - 1) * ts + dim));
 }
 
@@ -73,11 +77,10 @@ int check_cache(const qgemm_kv_cache* c, int act_dtype) {
   constexpr int64_t kMost = int64_t(1) << 40;
   if (c->token_stride < c->head_dim || c->token_stride > kMaxTokenStride || c->token_stride % step != 0)
     return QGEMM_ERR_ALIGN;
-  if (c->head_stride < 0 || c->head_stride > kMost || c->head_stride % step != 0 ||
-      (c->kv_heads > 1 && c->head_stride < c->head_dim))
+  if (!valid_step(c->kv_heads, c->head_stride, step, kMost) || (c->kv_heads > 1 && c->head_stride < c->head_dim))
     return QGEMM_ERR_ALIGN;
   // 2^31 pages of 2^30 elements stay below 2^62
-  if (c->page_stride < 0 || c->page_stride > (int64_t(1) << 30) || c->page_stride % step != 0) return QGEMM_ERR_ALIGN;
+  if (!valid_step(c->num_pages, c->page_stride, step, int64_t(1) << 30)) return QGEMM_ERR_ALIGN;
   return QGEMM_OK;
 }
 
@@ -261,8 +264,8 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
   if (!aligned(g.q, 16) || !aligned(g.out, 16) || !aligned(g.seq_lens, 4) || !aligned(g.block_table, 4) ||
       !aligned(q_start, 4))
     return QGEMM_ERR_ALIGN;
-  if (!valid_strides(g.q_token_stride, g.q_head_stride, g.q_heads, c->head_dim) ||
-      !valid_out_strides(num_tokens, g.out_token_stride, g.out_head_stride, g.q_heads, c->head_dim))
+  if (!valid_strides(num_tokens, g.q_token_stride, g.q_heads, g.q_head_stride, c->head_dim) ||
+      !valid_out_strides(num_tokens, g.out_token_stride, g.q_heads, g.out_head_stride, c->head_dim))
     return QGEMM_ERR_ALIGN;
   if (g.table_stride < 0 || g.table_stride > kMaxLen || g.max_len > g.table_stride * c->page_size)
     return QGEMM_ERR_SHAPE;
@@ -359,10 +362,10 @@ int run_append(const qgemm_append_call& g) {
   for (const void* p : {g.q, g.k, g.v, g.q_norm, g.k_norm, (const void*)g.rope, (const void*)g.q_out})
     if (!aligned(p, 16)) return QGEMM_ERR_ALIGN;
   if (!aligned(g.positions, 4) || !aligned(g.token_seq, 4) || !aligned(g.block_table, 4)) return QGEMM_ERR_ALIGN;
-  if (!valid_strides(g.q_token_stride, g.q_head_stride, g.q_heads, c->head_dim) ||
-      !valid_strides(g.k_token_stride, g.k_head_stride, c->kv_heads, c->head_dim) ||
-      !valid_strides(g.v_token_stride, g.v_head_stride, c->kv_heads, c->head_dim) ||
-      !valid_out_strides(g.num_tokens, g.out_token_stride, g.out_head_stride, g.q_heads, c->head_dim))
+  if (!valid_strides(g.num_tokens, g.q_token_stride, g.q_heads, g.q_head_stride, c->head_dim) ||
+      !valid_strides(g.num_tokens, g.k_token_stride, c->kv_heads, g.k_head_stride, c->head_dim) ||
+      !valid_strides(g.num_tokens, g.v_token_stride, c->kv_heads, g.v_head_stride, c->head_dim) ||
+      !valid_out_strides(g.num_tokens, g.out_token_stride, g.q_heads, g.out_head_stride, c->head_dim))
     return QGEMM_ERR_ALIGN;
   const int64_t D = c->head_dim;
   const Extent eq = extent3(g.q, g.num_tokens, g.q_token_stride, g.q_heads, g.q_head_stride, D);

@@ -335,7 +335,8 @@ int qgemm_w4a16_noalloc(const void* A, int64_t lda, const void* packed, void* C,
  *
  * Strides of q, k, v, q_out and out are in elements: head h of token t starts at
  * t * token_stride + h * head_stride, with head_dim values contiguous, 16-byte
- * aligned; so the parts of one fused product's output serve without a copy.
+ * aligned; so the parts of one fused product's output serve without a copy. A
+ * stride along which there is one token, head or page is not used.
  * act_dtype is QGEMM_DT_F16 or QGEMM_DT_BF16. q_heads is a multiple of kv_heads
  * of at most 128 times it: query head h reads key-value head
  * h / (q_heads / kv_heads). num_seqs and num_tokens are at most 65535 and 2^20

@@ -48,3 +48,19 @@ def test_long_contexts_stay_split_under_any_mask_that_shows_them():
     for window, sinks in ((0, 0), (131072, 0), (WINDOW_MAX, 0), (4096, 131072), (4096, SINKS_MAX), (1, SINKS_MAX)):
         dec, pre = _sizes(SHAPES[0], window, sinks)
         assert dec > 0 and pre > 0, (window, sinks)
+
+
+def test_strides_along_one_token_head_or_page_are_not_used():
+    import torch
+    from test_attn_abi_cpu import DEV, FP8, HIP, _append, _cache, _decode, _prefill
+
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not a device's")
+    one = dict(num_pages=1, page_stride=-3, kv_heads=1, head_stride=1)
+    for cache in (_cache(**one), _cache(**one, dtype=FP8)):
+        for odd in (1, -1, 7, (1 << 40) + 1):
+            assert _decode(cache, seqs=1, heads=1, cols=1, max_len=16, qts=odd, qhs=odd, ots=odd, ohs=odd) in (HIP, DEV)
+            assert _prefill(cache, seqs=1, tokens=1, heads=1, cols=1, max_len=16, qts=odd, qhs=odd, ots=odd,
+                            ohs=odd) in (HIP, DEV)
+            assert _append(cache, tokens=1, heads=1, cols=1, qts=odd, qhs=odd, kts=odd, khs=odd, vts=odd, vhs=odd,
+                           ots=odd, ohs=odd) in (HIP, DEV)

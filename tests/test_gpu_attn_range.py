@@ -245,3 +245,25 @@ def test_append_of_many_heads():
         assert not bool(buf[0].any())
         for p in range(16):
             assert torch.equal(buf[1, p], new[0] if p in kept.values() else torch.zeros_like(new[0])), p
+
+
+def test_strides_along_one_token_or_head():
+    _say("odd strides of single tokens and heads")
+    rng = np.random.default_rng(47)
+    D, act = 64, "f16"
+    pg = Paged(rng, [37], 1, D, act, 16, DEV)
+    bits, q = _values(rng, (1, 1, D), act)
+    plain = to_torch(bits, act, DEV)
+    odd = plain.as_strided((1, 1, D), (3, 1, 1))
+    out = torch.zeros(D, dtype=torch.float16, device=DEV).as_strided((1, 1, D), (5, 7, 1))
+    ref = _decode_refs(pg, q, np.float32(1 / 8).astype(np.float64))
+    start = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    for got in (_decode(pg, odd), _decode(pg, odd, out=out),
+                qg.attn_prefill(odd, pg.cache, pg.table_dev, start, pg.lens_dev, 1, 37)):
+        torch.cuda.synchronize()
+        check(oa.decode(to_bits(got), act), ref, act, PREFILL_WEIGHTS[act], "odd")
+    pos = torch.tensor([20], dtype=torch.int32, device=DEV)
+    got = qg.qk_rope_append(odd, odd, odd, pos, pg.cache, pg.table_dev, out=out)
+    torch.cuda.synchronize()
+    page, place = int(pg.table[0, 1]), 4
+    assert torch.equal(got, plain) and torch.equal(pg.k[page, place], plain[0]) and torch.equal(pg.v[page, place], plain[0])
