@@ -40,7 +40,8 @@ def _dtypes():
 class KVCache:
     """A paged key-value cache: k and v are [pages][page_size][kv_heads][head_dim] tensors (or views with the last
     dimension contiguous, the same strides for both), float16, bfloat16 or float8_e4m3fn; an e4m3 code stands for its
-    value times k_scale (keys) or v_scale (values). Holds references, copies nothing."""
+    value times k_scale (keys) or v_scale (values). Holds references, copies nothing, and is fixed: the calls take its
+    addresses, strides and scales as they were given here, so other ones need another KVCache (5 us)."""
 
     def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
@@ -65,6 +66,11 @@ class KVCache:
                                     self.page_size, self.kv_heads, self.head_dim, _dtypes()[k.dtype], self.k_scale,
                                     self.v_scale)
         self._address = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):
+        if "_address" in self.__dict__:
+            raise AttributeError(f"a KVCache is fixed: make a new one to change {name}")
+        super().__setattr__(name, value)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype, device, k_scale: float = 1.0,
@@ -227,7 +233,8 @@ def attn_decode(q, cache: KVCache, block_table, seq_lens, max_len: int, scale: f
                 sinks: int = 0, out=None, workspace: Workspace | None = None):
     """Attention of one new token per sequence over its cached tokens (its own included): q [sequences][q_heads]
     [head_dim], block_table int32 [sequences][columns], seq_lens int32 [sequences], all at most max_len (a host number,
-    so that the call reads nothing back). window > 0 shows the last `window` tokens and the first `sinks`. scale
+    so that the call reads nothing back; it sizes the grid and the workspace, so steps of a growing length do best with
+    one bound for many of them, rounded up). window > 0 shows the last `window` tokens and the first `sinks`. scale
     defaults to head_dim ** -0.5. Returns q's shape and type."""
     shape, dt, out, qa, oa = _queries(q, cache, out)
     B, H, D = shape

@@ -267,3 +267,12 @@ def test_strides_along_one_token_or_head():
     torch.cuda.synchronize()
     page, place = int(pg.table[0, 1]), 4
     assert torch.equal(got, plain) and torch.equal(pg.k[page, place], plain[0]) and torch.equal(pg.v[page, place], plain[0])
+
+
+def test_a_cache_object_is_fixed():
+    _say("fixed cache")
+    cache = qg.KVCache.empty(2, 16, 1, 64, torch.float8_e4m3fn, DEV, 0.5, 0.25)
+    for name, value in (("k_scale", 1.0), ("v_scale", 1.0), ("k", cache.v), ("v", cache.k), ("num_pages", 1)):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, value)
+    assert (cache.k_scale, cache.v_scale) == (0.5, 0.25)
