@@ -8,9 +8,10 @@
 // meet once at the end; parts meet in the last workgroup to arrive.
 //
 // Every byte of K and V is used once, so the kernel is bound by the cache's
-// stream: 256 contexts of 8192 tokens, 8 heads of 128, bf16, take 1220 us (7.0 TB/s),
-// one of 131072 in e4m3 46 us (5.8 TB/s), 32 of up to 4096 60 us (4.5 TB/s; parts of
-// uneven length). Short contexts are bound by the chain of launch, length, table
+// stream: 256 contexts of 8192 tokens, 8 heads of 128, bf16, take 1220 to 1330 us by
+// device (6.5 to 7.0 TB/s; a bare streaming read of 2 GiB, which has less to spread its
+// start and end over, reaches 6.2, a copy 4.9 read and written), one of 131072 in e4m3
+// 46 us (5.8 TB/s), 32 of up to 4096 60 us (4.5 TB/s; parts of uneven length). Short contexts are bound by the chain of launch, length, table
 // entry, load, join: 1 x 1000 tokens 9.7 us in parts, 12 x 256 7.8 us in one. Loads go
 // straight to registers in operand form; through LDS they would cost a barrier per
 // pair and bring no reuse:

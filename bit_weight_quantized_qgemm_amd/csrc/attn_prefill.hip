@@ -30,10 +30,12 @@
 // accumulators stay fp32.
 //
 // Bound by the matrix unit and, with it, by power: 8192 tokens, 64/8 heads of 128,
-// bf16, take 1020 us (1075 TFLOP/s; a library product of 8192^3 reaches 1230), at
-// 1.95 GHz of 2.4 and with the matrix unit busy in 53 % of the cycles. 64 rows per
+// bf16, take 1010 to 1040 us by device (1057 to 1090 TFLOP/s; a library product of
+// 8192^3 reaches 1230 to 1250), at 1.95 GHz of 2.4 and with the matrix unit busy in 53 % of the cycles. 64 rows per
 // wave took 1058 us on a device where this takes 1026, eight waves per workgroup 1011
-// (but 512 tokens on 4096 then take 108 us instead of 77). A window of 1024 tokens
+// (but 512 tokens on 4096 then take 108 us instead of 77). Other heads, 4096 tokens of
+// 32/8: 80 values 118 to 130 us (660 to 730 TFLOP/s), 96 123 to 127, 192 267 to 274;
+// 16/8 of 256 161 to 168. A window of 1024 tokens
 // leaves 17 turns per workgroup: 162 us for 8192 tokens of 32/8 heads, e4m3, of which
 // a workgroup's start and end take 8 of 41 us.
 #include "attn_device.h"
