@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_de
     float top = t[0];
 #pragma unroll
     for (int r = 1; r < 8; ++r) top = fmaxf(top, t[r]);
-    if (__any(top > mref + PF::kSlack)) {
+    if (__any(top > raise_limit<PF>(mref))) {
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = fmaxf(mref, top);

@@ -16,7 +16,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // matrix instructions.
 struct F16 {
   using T = f16;
-  static constexpr float kLift = 11.0f, kSlack = 4.0f;   // of softmax weights, below
+  static constexpr float kLift = 11.0f, kSlack = 4.0f, kShrink = 0x1p-20f;   // of softmax weights, below
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const f32x2 x = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16x2));
@@ -41,7 +41,7 @@ struct F16 {
 };
 struct BF16 {
   using T = bf16;
-  static constexpr float kLift = 0.0f, kSlack = 8.0f;
+  static constexpr float kLift = 0.0f, kSlack = 8.0f, kShrink = 0.0f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const f32x2 x = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
@@ -76,8 +76,17 @@ constexpr float kNegInf = -__builtin_huge_valf();
 //          the reference's weight. Without lift, a first token 18 nats above 20000
 //          others took them nearly all away. At a slack of 8 the lift is at most 7 and
 //          2^-32 the end, at the same speed (prefill of 4 prompts up to 2048 tokens,
-//          32 heads: 104.7 us, here 105.2; every other case the same).
+//          32 heads: 104.7 us, here 105.2; every other case the same). The step from
+//          2^15 to the type's end is one bit, and a score of 2^24 or more is itself off
+//          by that much in fp32, so the slack shrinks with the reference, to none at
+//          2^22: weights stay finite up to scores of 2^25.
 
+// The score above which a row's reference moves.
+template <class PF>
+__device__ __forceinline__ float raise_limit(float mref) {
+  if constexpr (PF::kShrink == 0.f) return mref + PF::kSlack;
+  else return __builtin_fmaf(-PF::kShrink, fabsf(mref), mref + PF::kSlack);
+}
 // What a row's scores are taken from, by its reference.
 template <class PF>
 __device__ __forceinline__ float weight_base(float mref) {

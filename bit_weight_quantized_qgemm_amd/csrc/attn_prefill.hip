@@ -388,7 +388,7 @@ __device__ __forceinline__ void prefill_body(const AttnArgs& p, char* lds) {
     return top * p.scale_log2;
   };
   auto raise = [&](float top) {   // moves the reference maxima, if scores pass them
-    if (__builtin_expect(__any(top > mref + PF::kSlack), 0)) {
+    if (__builtin_expect(__any(top > raise_limit<PF>(mref)), 0)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = fmaxf(mref, top);
       const float f = m == kNegInf ? 1.f : exp2_of(mref - m);

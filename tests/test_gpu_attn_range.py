@@ -276,3 +276,33 @@ def test_a_cache_object_is_fixed():
         with pytest.raises(AttributeError):
             setattr(cache, name, value)
     assert (cache.k_scale, cache.v_scale) == (0.5, 0.25)
+
+
+@pytest.mark.parametrize("act,cache", [("f16", "f16"), ("f16", "fp8"), ("bf16", "bf16")])
+def test_scores_that_fp32_hardly_tells_apart(act, cache):
+    _say("scores of 2^24", act, cache)
+    # about 2^24.7 in log2 units and within 20 of one another: which token wins is up to fp32, but every output is a
+    # mean of the values
+    rng = np.random.default_rng(48)
+    n, H, D = 512, 4, 128
+    k = np.full((n, 1, D), 96.0)
+    k[:, 0, 0] = np.arange(n) * 9 // n   # scores that creep past the first ones
+    v = rng.standard_normal((n, 1, D))
+    q = np.full((1, H, D), 1024.0)
+    q[0, :, 0] = [1, 1.5, -1, 0.75]
+    kb, vb = oa.encode(k, cache), oa.encode(v, cache)
+    v = oa.decode(vb, cache)[:, 0]
+    place = [to_torch(x.reshape(n // 16, 16, 1, D), cache, DEV) for x in (kb, vb)]
+    pg = qg.KVCache(*place)
+    table = torch.arange(n // 16, dtype=torch.int32, device=DEV)[None]
+    lens, start = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([n], [0, 1]))
+    qd = to_torch(oa.encode(q, act), act, DEV)
+    slop = 2 * oa.ROUNDOFF[act] * np.abs(v).max(axis=0)
+    for splits in (1, 3):
+        qg.set_attn_splits(splits)
+        for out in (qg.attn_decode(qd, pg, table, lens, n, scale=1.5),
+                    qg.attn_prefill(qd, pg, table, start, lens, 1, n, scale=1.5)):
+            torch.cuda.synchronize()
+            got = oa.decode(to_bits(out), act)[0]
+            assert np.isfinite(got).all(), splits
+            assert np.all(got <= v.max(axis=0) + slop) and np.all(got >= v.min(axis=0) - slop), splits
