@@ -37,34 +37,34 @@ def _attend(name, op, seqs, groups, q_len, shared, own_len, heads, kv_heads, dim
 def listed():
     return [
         # one request's next token through a square projection: a call whose latency counts
-        _lora("lora 1 token, 4096 to 4096, rank 16", 1, 4096, [4096], 16, 1, "f16", pool=8),
+        _lora("lora 1 token 4096 to 4096 rank 16", 1, 4096, [4096], 16, 1, "f16", pool=8),
         # a decoding batch in which every request has its own adapter, on the fused q/k/v product
-        _lora("lora 64 tokens of 64 adapters, fused q/k/v, rank 16", 64, 8192, [8192, 1024, 1024], 16, 64, "bf16"),
+        _lora("lora 64 tokens of 64 adapters fused q/k/v rank 16", 64, 8192, [8192, 1024, 1024], 16, 64, "bf16"),
         # a decoding batch of adapters of different ranks, in no order, some requests without one, on a wide projection
-        _lora("lora 128 tokens of 24 adapters, ranks to 64", 128, 8192, [28672], 64, 24, "f16", mixed=True, none=True),
+        _lora("lora 128 tokens of 24 adapters ranks to 64", 128, 8192, [28672], 64, 24, "f16", mixed=True, none=True),
         # a ragged batch of prompts
-        _lora("lora 1003 tokens of 5 prompts, 4096 to 11008", 1003, 4096, [11008], 64, 5, "f16", prompts=True),
+        _lora("lora 1003 tokens of 5 prompts 4096 to 11008", 1003, 4096, [11008], 64, 5, "f16", prompts=True),
         # long prompts
-        _lora("lora 8192 tokens of 3 prompts, 8192 to 8192", 8192, 8192, [8192], 16, 3, "bf16", prompts=True),
+        _lora("lora 8192 tokens of 3 prompts 8192 to 8192", 8192, 8192, [8192], 16, 3, "bf16", prompts=True),
         # a few short requests behind one short prompt: latency
-        _attend("decode 4 on 768 shared, 32/32 heads", "decode", 4, 1, 1, 768, 130, 32, 32, 128, "f16", "f16"),
+        _attend("decode 4 on 768 shared 32/32 heads", "decode", 4, 1, 1, 768, 130, 32, 32, 128, "f16", "f16"),
         # a serving batch behind one long system prompt, eight query heads to a key-value head
-        _attend("decode 64 on 8192 shared, 64/8 heads", "decode", 64, 1, 1, 8192, 512, 64, 8, 128, "bf16", "bf16",
+        _attend("decode 64 on 8192 shared 64/8 heads", "decode", 64, 1, 1, 8192, 512, 64, 8, 128, "bf16", "bf16",
                 ragged=True),
         # several system prompts of different lengths at once, some requests without one, 8-bit cache
-        _attend("decode 96 in 4 groups, 32/8 heads, fp8 cache", "decode", 96, 4, 1, 4096, 700, 32, 8, 128, "bf16", "fp8",
+        _attend("decode 96 in 4 groups 32/8 heads fp8 cache", "decode", 96, 4, 1, 4096, 700, 32, 8, 128, "bf16", "fp8",
                 page=32, ragged=True, loners=5),
         # unshared heads: every sequence's cache is large, one row of it for each
-        _attend("decode 128 on 2048 shared, 32/32 heads", "decode", 128, 1, 1, 2048, 256, 32, 32, 128, "f16", "f16",
+        _attend("decode 128 on 2048 shared 32/32 heads", "decode", 128, 1, 1, 2048, 256, 32, 32, 128, "f16", "f16",
                 ragged=True),
         # a few speculated tokens per sequence
-        _attend("prefill 16 x 5 on 6000 shared, 64/8 heads", "prefill", 16, 1, 5, 6000, 100, 64, 8, 128, "bf16", "bf16",
+        _attend("prefill 16 x 5 on 6000 shared 64/8 heads", "prefill", 16, 1, 5, 6000, 100, 64, 8, 128, "bf16", "bf16",
                 ragged=True),
         # ragged questions behind one prompt, heads of 80
-        _attend("prefill 24 ragged on 2048 shared, 32/32 heads of 80", "prefill", 24, 1, 200, 2048, 200, 32, 32, 80,
+        _attend("prefill 24 ragged on 2048 shared 32/32 heads of 80", "prefill", 24, 1, 200, 2048, 200, 32, 32, 80,
                 "f16", "f16", ragged=True),
         # chunks of 128 tokens behind a very long document, 8-bit cache
-        _attend("prefill 32 x 128 on 16384 shared, fp8 cache", "prefill", 32, 1, 128, 16384, 128, 32, 8, 128, "bf16",
+        _attend("prefill 32 x 128 on 16384 shared fp8 cache", "prefill", 32, 1, 128, 16384, 128, 32, 8, 128, "bf16",
                 "fp8", page=64),
     ]
 
