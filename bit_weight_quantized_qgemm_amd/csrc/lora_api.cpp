@@ -1,0 +1,218 @@
+// C-ABI front end of the low-rank adapters: argument validation (before any HIP
+// call), the work decomposition and kernel dispatch. See include/qgemm.h for the
+// contract.
+#include "qgemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "lora_internal.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxStride = int64_t(1) << 32;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A tensor's bytes in memory: [first, last).
+struct Extent {
+  uintptr_t first = 0, last = 0;
+};
+bool overlap(const Extent& a, const Extent& b) { return a.first < b.last && b.first < a.last; }
+Extent extent(const void* p, int64_t elems, int64_t elt) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return p && elems > 0 ? Extent{a, a + (uintptr_t)(elems * elt)} : Extent{};
+}
+Extent extent2(const void* p, int64_t rows, int64_t stride, int64_t cols) {
+  return extent(p, (rows - 1) * stride + cols, 2);
+}
+
+int check_counts(int64_t num_tokens, int64_t num_adapters) {
+  if (num_tokens < 0 || num_tokens > qg::kMaxLoraTokens) return QGEMM_ERR_SHAPE;
+  if (num_adapters < 1 || num_adapters > qg::kMaxLoraAdapters) return QGEMM_ERR_SHAPE;
+  return QGEMM_OK;
+}
+
+int check_shape(int64_t K, int64_t N, int32_t rank, int32_t slices) {
+  if (K < 8 || K > kMaxDim || K % 8 != 0 || N < 8 || N > kMaxDim || N % 8 != 0) return QGEMM_ERR_SHAPE;
+  if (rank < 8 || rank > qg::kMaxLoraRank || rank % 8 != 0) return QGEMM_ERR_SHAPE;
+  if (slices < 1 || slices > QGEMM_LORA_MAX_SLICES) return QGEMM_ERR_SHAPE;
+  return QGEMM_OK;
+}
+
+// A stride of rows of `cols` elements; not used where there is one row.
+bool valid_stride(int64_t rows, int64_t stride, int64_t cols) {
+  return rows == 1 || (stride >= cols && stride <= kMaxStride && stride % 8 == 0);
+}
+
+qg::LoraDecomposition decompose(int64_t tokens, int64_t adapters, int64_t K, int32_t rank, int32_t slices) {
+  qg::LoraDecomposition d;
+  const qg::LoraPlanLayout l = qg::lora_plan_layout(tokens, adapters);
+  d.wide = tokens > 256;
+  d.cap = d.wide ? l.cap64 : l.cap16;
+  d.rank_tiles = (rank + qg::kLoraRankTile - 1) / qg::kLoraRankTile;
+  const int64_t tiles = (int64_t)slices * d.rank_tiles;
+  d.chunk_tiles = tiles >= 3 ? 4 : (int)tiles;
+  d.chunks = (int)((tiles + d.chunk_tiles - 1) / d.chunk_tiles);
+  // Parts of K: about two workgroups per compute unit, as far as the parts' sums stay a
+  // quarter of x's bytes and each of a workgroup's four waves keeps 32 of K.
+  const int64_t want = 2 * qg::device_cu_count() / std::max<int64_t>(1, d.cap * d.chunks);
+  const int64_t most = std::min<int64_t>({(K + 127) / 128, std::max<int64_t>(1, K / (8 * tiles * 16)), 32});
+  const int64_t splits = std::max<int64_t>(1, std::min(want, most));
+  d.split_k = (int)(((K + splits - 1) / splits + 127) / 128 * 128);
+  d.splits = (int)((K + d.split_k - 1) / d.split_k);
+  d.partial_offset = qg::kCounterBytes;
+  d.ws_bytes = d.partial_offset + (size_t)d.splits * tokens * tiles * 16 * 4;
+  return d;
+}
+
+int run_lora(const qgemm_lora_call& g) {
+  const qgemm_lora_adapters* w = g.adapters;
+  if (!w) return QGEMM_ERR_NULL;
+  if (w->dtype != QGEMM_DT_F16 && w->dtype != QGEMM_DT_BF16) return QGEMM_ERR_RANGE;
+  int st = check_counts(g.num_tokens, w->num_adapters);
+  if (st) return st;
+  st = check_shape(w->K, w->N, w->rank, w->slices);
+  if (st) return st;
+  int64_t columns = 0;
+  for (int i = 0; i < w->slices; ++i) {
+    if (w->widths[i] < 8 || w->widths[i] > w->N || w->widths[i] % 8 != 0) return QGEMM_ERR_SHAPE;
+    columns += w->widths[i];
+  }
+  if (columns != w->N) return QGEMM_ERR_SHAPE;
+  if (!w->a || !w->b) return QGEMM_ERR_NULL;
+  if (!aligned(w->a, 16) || !aligned(w->b, 16) || !aligned(w->scales, 4) || !aligned(w->ranks, 4)) return QGEMM_ERR_ALIGN;
+  const int64_t a_elems = (int64_t)w->slices * w->rank * w->K, b_elems = w->N * w->rank;
+  if (!valid_stride(w->num_adapters, w->a_stride, a_elems) || !valid_stride(w->num_adapters, w->b_stride, b_elems))
+    return QGEMM_ERR_ALIGN;
+  if (g.num_tokens == 0) return QGEMM_OK;
+  if (!g.x || !g.out || !g.plan) return QGEMM_ERR_NULL;
+  if (!aligned(g.x, 16) || !aligned(g.out, 16) || !aligned(g.base, 16) || !aligned(g.plan, 16)) return QGEMM_ERR_ALIGN;
+  if (!valid_stride(g.num_tokens, g.x_stride, w->K) || !valid_stride(g.num_tokens, g.out_stride, w->N) ||
+      (g.base && !valid_stride(g.num_tokens, g.base_stride, w->N)))
+    return QGEMM_ERR_ALIGN;
+  const qg::LoraPlanLayout l = qg::lora_plan_layout(g.num_tokens, w->num_adapters);
+  if (g.plan_bytes != (size_t)l.words * 4) return QGEMM_ERR_SIZE;
+  const qg::LoraDecomposition d = decompose(g.num_tokens, w->num_adapters, w->K, w->rank, w->slices);
+  if (!g.workspace) return QGEMM_ERR_NULL;
+  if (g.workspace_bytes < d.ws_bytes) return QGEMM_ERR_WORKSPACE;
+  if (!aligned(g.workspace, 16)) return QGEMM_ERR_ALIGN;
+  const Extent out = extent2(g.out, g.num_tokens, g.out_stride, w->N);
+  const Extent base = extent2(g.base, g.num_tokens, g.base_stride, w->N);
+  const Extent ws = extent(g.workspace, (int64_t)d.ws_bytes, 1);
+  const bool in_place = g.base == g.out && (g.num_tokens == 1 || g.base_stride == g.out_stride);
+  if (g.base && !in_place && overlap(out, base)) return QGEMM_ERR_ALIAS;
+  const Extent others[] = {extent2(g.x, g.num_tokens, g.x_stride, w->K),
+                           extent2(w->a, w->num_adapters, w->a_stride, a_elems),
+                           extent2(w->b, w->num_adapters, w->b_stride, b_elems),
+                           extent(w->scales, w->num_adapters, 4),
+                           extent(w->ranks, w->num_adapters, 4),
+                           extent(g.plan, (int64_t)g.plan_bytes, 1)};
+  for (const Extent& e : others)
+    if (overlap(out, e) || overlap(ws, e)) return QGEMM_ERR_ALIAS;
+  if (overlap(ws, out) || overlap(ws, base)) return QGEMM_ERR_ALIAS;
+  st = qg::check_current_device();
+  if (st) return st;
+
+  qg::LoraArgs a{};
+  a.x = g.x;
+  a.a = w->a;
+  a.b = w->b;
+  a.base = g.base;
+  a.out = g.out;
+  a.x_stride = g.x_stride;
+  a.base_stride = g.base_stride;
+  a.out_stride = g.out_stride;
+  a.a_stride = w->a_stride;
+  a.b_stride = w->b_stride;
+  a.scales = w->scales;
+  a.ranks = w->ranks;
+  a.plan = static_cast<const int32_t*>(g.plan);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + d.partial_offset);
+  a.tokens = (int32_t)g.num_tokens;
+  a.adapters = w->num_adapters;
+  a.k = (int32_t)w->K;
+  a.n = (int32_t)w->N;
+  a.rank = w->rank;
+  a.slices = w->slices;
+  a.tiles_at = (int32_t)(d.wide ? l.tiles64 : l.tiles16);
+  a.cap = (int32_t)d.cap;
+  a.wide = d.wide;
+  a.rank_tiles = d.rank_tiles;
+  a.splits = d.splits;
+  a.split_k = d.split_k;
+  a.chunks = d.chunks;
+  a.in_place = g.base && in_place;
+  // Columns: each wave takes up to eight tiles of 64, fewer where that would leave less
+  // than 16 waves per compute unit; more where the grid would pass 2^22 workgroups.
+  const int64_t col_tiles = (w->N + qg::kLoraCols - 1) / qg::kLoraCols;
+  int64_t each = d.cap * col_tiles / (16 * qg::device_cu_count());
+  each = std::max<int64_t>(1, std::min<int64_t>(each, 8));
+  while (d.cap * (col_tiles / (qg::kLoraWaves * each) + w->slices) > (int64_t(1) << 20)) each *= 2;
+  a.group_cols = (int32_t)(qg::kLoraWaves * each);
+  for (int i = 0; i < w->slices; ++i) {
+    const int64_t tiles = (w->widths[i] + qg::kLoraCols - 1) / qg::kLoraCols;
+    a.col_begin[i + 1] = a.col_begin[i] + (int32_t)w->widths[i];
+    a.group_begin[i + 1] = a.group_begin[i] + (int32_t)((tiles + a.group_cols - 1) / a.group_cols);
+  }
+  const bool bf16 = w->dtype == QGEMM_DT_BF16;
+  hipStream_t s = static_cast<hipStream_t>(g.stream);
+  hipError_t e = qg::launch_lora_shrink(a, bf16, d.chunk_tiles, s);
+  if (e == hipSuccess) e = qg::launch_lora_expand(a, bf16, s);
+  if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
+  return QGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qgemm_lora_plan_bytes(int64_t num_tokens, int64_t num_adapters, size_t* bytes) {
+  if (!bytes) return QGEMM_ERR_NULL;
+  const int st = check_counts(num_tokens, num_adapters);
+  if (st) return st;
+  *bytes = (size_t)qg::lora_plan_layout(num_tokens, num_adapters).words * 4;
+  return QGEMM_OK;
+}
+
+int qgemm_lora_plan(const int32_t* ids, int64_t num_tokens, int64_t num_adapters, void* plan, size_t plan_bytes,
+                    void* stream) {
+  int st = check_counts(num_tokens, num_adapters);
+  if (st) return st;
+  if (num_tokens == 0) return QGEMM_OK;
+  if (!ids || !plan) return QGEMM_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(plan, 16)) return QGEMM_ERR_ALIGN;
+  const qg::LoraPlanLayout l = qg::lora_plan_layout(num_tokens, num_adapters);
+  if (plan_bytes != (size_t)l.words * 4) return QGEMM_ERR_SIZE;
+  if (overlap(extent(ids, num_tokens, 4), extent(plan, (int64_t)plan_bytes, 1))) return QGEMM_ERR_ALIAS;
+  st = qg::check_current_device();
+  if (st) return st;
+  qg::LoraPlanArgs a{};
+  a.ids = ids;
+  a.plan = static_cast<int32_t*>(plan);
+  a.tokens = (int32_t)num_tokens;
+  a.adapters = (int32_t)num_adapters;
+  a.tiles16 = (int32_t)l.tiles16;
+  a.tiles64 = (int32_t)l.tiles64;
+  const hipError_t e = qg::launch_lora_plan(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
+  return QGEMM_OK;
+}
+
+int qgemm_lora_workspace_bytes(int64_t num_tokens, int64_t num_adapters, int64_t K, int64_t N, int32_t rank,
+                               int32_t slices, size_t* bytes) {
+  if (!bytes) return QGEMM_ERR_NULL;
+  int st = check_counts(num_tokens, num_adapters);
+  if (st) return st;
+  st = check_shape(K, N, rank, slices);
+  if (st) return st;
+  *bytes = num_tokens == 0 ? 0 : decompose(num_tokens, num_adapters, K, rank, slices).ws_bytes;
+  return QGEMM_OK;
+}
+
+int qgemm_lora(const qgemm_lora_call* call) { return call ? run_lora(*call) : QGEMM_ERR_NULL; }
+
+}  // extern "C"

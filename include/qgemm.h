@@ -9,7 +9,8 @@
  * a general-grid 4-bit variant (qgemm_w4g) and a bit-plane W_b A8 format
  * (qgemm_bitplane_*), both below; and, next to these products, what attention
  * needs around a paged key-value cache (qgemm_qk_rope_append, qgemm_attn_decode,
- * qgemm_attn_prefill; their types, shapes and strides stand with them):
+ * qgemm_attn_prefill; their types, shapes and strides stand with them) and low-rank
+ * adapters of many requests beside a product (qgemm_lora):
  *
  *   W4A16  fp16 activations; unsigned 4-bit codes q (0..15) with an implicit
  *          zero point 8 and one fp16 scale s per group of 128 consecutive k of
@@ -502,6 +503,80 @@ int qgemm_attn_prefill_call(const qgemm_attn_call* call);
  * qgemm_set_plan_override; affects the attention workspace queries too.
  */
 int qgemm_attn_set_splits(int splits);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[t] = base[t] + s[a] * B[a] (A[a] x[t]),  a = the adapter of row t;
+ * a row without one keeps its base (zeros where base is NULL).
+ *
+ * The projection's N columns are cut into `slices` runs of widths[i] columns (a fused
+ * q/k/v product has three, otherwise there is one), each with a first matrix of its
+ * own: columns of slice i use A[a][i].
+ *   a        [num_adapters][slices][rank][K]  (dtype), adapters a_stride elements apart
+ *   b        [num_adapters][N][rank]          (dtype), adapters b_stride elements apart
+ *   scales   fp32 [num_adapters] or NULL (1)
+ *   ranks    int32 [num_adapters] or NULL: adapter a has the ranks 0..ranks[a]-1, taken
+ *            as 0..rank and up to a whole multiple of 8; others are not used, whatever
+ *            their memory holds
+ *   K, N     multiples of 8, 8..2^20; widths multiples of 8, their sum N
+ *   rank     a multiple of 8, 8..256; num_adapters 1..4096
+ *   dtype    QGEMM_DT_F16 or QGEMM_DT_BF16: of a, b, x, base and out
+ * Matrices are 16-byte aligned, strides multiples of 8; a stride along which there is
+ * one adapter or row is not used.
+ */
+#define QGEMM_LORA_MAX_SLICES 8
+typedef struct qgemm_lora_adapters {
+  const void* a;
+  const void* b;
+  int64_t a_stride, b_stride;
+  const float* scales;
+  const int32_t* ranks;
+  int64_t K, N;
+  int64_t widths[QGEMM_LORA_MAX_SLICES];
+  int32_t num_adapters, rank, slices, dtype;
+} qgemm_lora_adapters;
+
+/*
+ * The plan of a batch: its rows sorted by adapter, which every projection of every
+ * layer can use while the batch stays the same. ids is int32 [num_tokens]; an id
+ * outside 0..num_adapters-1 stands for no adapter. plan holds exactly
+ * qgemm_lora_plan_bytes() bytes, 16-byte aligned. Asynchronous on `stream`;
+ * num_tokens is 0..65535.
+ */
+int qgemm_lora_plan_bytes(int64_t num_tokens, int64_t num_adapters, size_t* bytes);
+int qgemm_lora_plan(const int32_t* ids, int64_t num_tokens, int64_t num_adapters, void* plan,
+                    size_t plan_bytes, void* stream);
+
+/*
+ * The product: x [num_tokens][x_stride], base (or NULL) and out [num_tokens] of their
+ * strides. out may be base itself (same stride; rows without an adapter are then left
+ * as they are); otherwise it must not overlap an input. num_tokens and
+ * adapters->num_adapters must be those of the plan (with a plan of others nothing is
+ * written). A x is summed in fp32, goes on as two 16-bit terms (good to 2^-22 of the
+ * row's largest, bf16 2^-16) and its product with B is summed in fp32; each output is
+ * rounded once. Rows do not influence each other, nor do the order of the ids; results
+ * do not change from run to run. The workspace (always needed) follows
+ * qgemm_workspace_bytes' contract; its counters are not touched.
+ */
+typedef struct qgemm_lora_call {
+  const qgemm_lora_adapters* adapters;
+  const void* x;
+  int64_t x_stride;
+  const void* plan;
+  size_t plan_bytes;
+  const void* base;
+  int64_t base_stride;
+  void* out;
+  int64_t out_stride;
+  int64_t num_tokens;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} qgemm_lora_call;
+
+int qgemm_lora_workspace_bytes(int64_t num_tokens, int64_t num_adapters, int64_t K, int64_t N,
+                               int32_t rank, int32_t slices, size_t* bytes);
+int qgemm_lora(const qgemm_lora_call* call);
 
 /*
  * Work decomposition used for a call of this shape (for tests and tuning).
