@@ -21,7 +21,8 @@ __all__ = [
     "packed_bytes_bitplane", "workspace_bytes_bitplane", "repack_bitplane", "bitplane_a8", "plan_info",
     "w4a16_noalloc", "DT_FP8", "KVCache", "rope_table", "qk_rope_append", "attn_decode", "attn_prefill",
     "set_attn_splits", "attn_decode_workspace_bytes", "attn_prefill_workspace_bytes",
-    "LoraAdapters", "LoraBatch", "lora", "lora_workspace_bytes",
+    "LoraAdapters", "LoraBatch", "lora", "lora_workspace_bytes", "attn_decode_shared", "attn_prefill_shared",
+    "set_attn_sharing", "attn_decode_shared_workspace_bytes", "attn_prefill_shared_workspace_bytes",
 ]
 
 FMT_W4A16 = 1
@@ -51,6 +52,8 @@ EXPORTED_SYMBOLS = (
     "qgemm_attn_prefill_workspace_bytes", "qgemm_attn_prefill", "qgemm_attn_set_splits",
     "qgemm_qk_rope_append_call", "qgemm_attn_decode_call", "qgemm_attn_prefill_call",
     "qgemm_lora_plan_bytes", "qgemm_lora_plan", "qgemm_lora_workspace_bytes", "qgemm_lora",
+    "qgemm_attn_decode_shared_workspace_bytes", "qgemm_attn_decode_shared",
+    "qgemm_attn_prefill_shared_workspace_bytes", "qgemm_attn_prefill_shared", "qgemm_attn_set_sharing",
 )
 
 
@@ -117,7 +120,14 @@ def lib() -> ctypes.CDLL:
         L.qgemm_lora_plan.argtypes = [vp, i64, i64, vp, ctypes.c_size_t, vp]
         L.qgemm_lora_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32, u64p]
         L.qgemm_lora.argtypes = [ctypes.c_char_p]   # the struct's bytes
+        L.qgemm_attn_decode_shared_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i32, i64, i64, u64p]
+        L.qgemm_attn_prefill_shared_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32, i32, i64, i32, i64, i64, u64p]
+        for name in ("qgemm_attn_decode_shared", "qgemm_attn_prefill_shared"):
+            getattr(L, name).argtypes = [ctypes.c_char_p]   # the struct's bytes
+        L.qgemm_attn_set_sharing.argtypes = [ctypes.c_int]
         for name in ("qgemm_lora_plan_bytes", "qgemm_lora_plan", "qgemm_lora_workspace_bytes", "qgemm_lora",
+                     "qgemm_attn_decode_shared_workspace_bytes", "qgemm_attn_decode_shared",
+                     "qgemm_attn_prefill_shared_workspace_bytes", "qgemm_attn_prefill_shared", "qgemm_attn_set_sharing",
                      "qgemm_qk_rope_append", "qgemm_attn_decode_workspace_bytes", "qgemm_attn_decode",
                      "qgemm_attn_prefill_workspace_bytes", "qgemm_attn_prefill", "qgemm_attn_set_splits",
                      "qgemm_packed_bytes", "qgemm_workspace_bytes", "qgemm_repack", "qgemm_w4a16",
@@ -488,8 +498,10 @@ def bitplane_a8(A_i8, a_scale, blob, K: int, N: int, bits: int, out=None, acc_ou
 
 
 # ----------------------------------------------------------------------------- attention
-from .attention import (KVCache, attn_decode, attn_decode_workspace_bytes, attn_prefill,  # noqa: E402
-                        attn_prefill_workspace_bytes, qk_rope_append, rope_table, set_attn_splits)
+from .attention import (KVCache, attn_decode, attn_decode_shared, attn_decode_shared_workspace_bytes,  # noqa: E402
+                        attn_decode_workspace_bytes, attn_prefill, attn_prefill_shared,
+                        attn_prefill_shared_workspace_bytes, attn_prefill_workspace_bytes, qk_rope_append, rope_table,
+                        set_attn_sharing, set_attn_splits)
 
 # ----------------------------------------------------------------------------- adapters of many requests
 from .lora import LoraAdapters, LoraBatch, lora, lora_workspace_bytes  # noqa: E402

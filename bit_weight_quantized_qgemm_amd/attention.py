@@ -1,5 +1,6 @@
 """Attention around a paged key-value cache: the binding of the ``qgemm_qk_rope_append``,
-``qgemm_attn_decode`` and ``qgemm_attn_prefill`` entry points of ``include/qgemm.h``.
+``qgemm_attn_decode`` and ``qgemm_attn_prefill`` entry points of ``include/qgemm.h``, and of
+``qgemm_attn_decode_shared`` and ``qgemm_attn_prefill_shared`` for batches that begin with the same tokens.
 
 As in the rest of the package: argument marshalling only, on the current HIP stream of the tensors'
 device, and no fallback. Shapes, types and devices are checked here; strides, alignment, ranges and
@@ -16,7 +17,8 @@ import struct
 from . import DT_BF16, DT_F16, DT_FP8, Workspace, _check, _default_ws, _torch, lib
 
 __all__ = ["KVCache", "rope_table", "qk_rope_append", "attn_decode", "attn_prefill", "set_attn_splits",
-           "attn_decode_workspace_bytes", "attn_prefill_workspace_bytes"]
+           "attn_decode_workspace_bytes", "attn_prefill_workspace_bytes", "attn_decode_shared", "attn_prefill_shared",
+           "set_attn_sharing", "attn_decode_shared_workspace_bytes", "attn_prefill_shared_workspace_bytes"]
 
 
 class _CacheStruct(ctypes.Structure):
@@ -28,6 +30,7 @@ class _CacheStruct(ctypes.Structure):
 # The argument structs of the *_call entry points, packed into bytes: one argument through ctypes costs about as much
 # as all of a struct's fields.
 _attn_call = struct.Struct("@P2q2PqPP4qqP2qPNP3if").pack
+_shared_call = struct.Struct("@P2q2PqPP4qqP2qPNP3if2P2q").pack   # the same and the groups
 _append_call = struct.Struct("@P2qP2qP2q3Pq3P3qPP2qP4if4x").pack
 
 
@@ -277,4 +280,92 @@ def attn_prefill(q, cache: KVCache, block_table, q_start, seq_lens, max_q: int, 
     status = lib().qgemm_attn_prefill_call(call)
     if status:
         _check(status, "qgemm_attn_prefill")
+    return out
+
+
+def set_attn_sharing(mode: int = 0):
+    """Compute shared tokens apart where that is worth it (0), always (1) or never (2); see include/qgemm.h."""
+    _check(lib().qgemm_attn_set_sharing(mode), "qgemm_attn_set_sharing")
+    _ws_sizes.clear()
+
+
+def attn_decode_shared_workspace_bytes(num_seqs: int, max_len: int, q_heads: int, kv_heads: int, head_dim: int,
+                                       window: int = 0, sinks: int = 0, num_groups: int = 0, max_shared: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().qgemm_attn_decode_shared_workspace_bytes(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks,
+                                                          num_groups, max_shared, ctypes.byref(out)),
+           "qgemm_attn_decode_shared_workspace_bytes")
+    return out.value
+
+
+def attn_prefill_shared_workspace_bytes(num_seqs: int, num_tokens: int, max_q: int, max_len: int, q_heads: int,
+                                        kv_heads: int, head_dim: int, window: int = 0, sinks: int = 0,
+                                        num_groups: int = 0, max_shared: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().qgemm_attn_prefill_shared_workspace_bytes(num_seqs, num_tokens, max_q, max_len, q_heads, kv_heads,
+                                                           head_dim, window, sinks, num_groups, max_shared,
+                                                           ctypes.byref(out)),
+           "qgemm_attn_prefill_shared_workspace_bytes")
+    return out.value
+
+
+def _groups(group_start, shared_lens, cache: KVCache):
+    """Checks the groups; returns (pointers, their number)."""
+    if len(shared_lens.shape) != 1:
+        raise ValueError("shared_lens must be [groups]")
+    groups = shared_lens.shape[0]
+    return _int32(group_start, "group_start", cache, (groups + 1,)), _int32(shared_lens, "shared_lens", cache, (groups,)), groups
+
+
+def attn_decode_shared(q, cache: KVCache, block_table, seq_lens, max_len: int, group_start, shared_lens, max_shared: int,
+                       scale: float | None = None, window: int = 0, sinks: int = 0, out=None,
+                       workspace: Workspace | None = None):
+    """``attn_decode`` for a batch whose sequences begin with the same tokens, group by group: the first shared_lens[g]
+    tokens of sequences group_start[g]..group_start[g+1]-1 lie in the same pages (which every sequence's table row names)
+    and are read and computed once for all of them. group_start int32 [groups + 1], nondecreasing, and shared_lens int32
+    [groups] on the device; sequences outside all groups share nothing. max_shared bounds shared_lens (a host number: more
+    is taken as max_shared). Keys and values of shared tokens have to be finite."""
+    shape, dt, out, qa, oa = _queries(q, cache, out)
+    B, H, D = shape
+    table, cols, seqs = _table(block_table, cache)
+    if B != seqs:
+        raise ValueError("q must have one row per sequence")
+    lens = _int32(seq_lens, "seq_lens", cache, (B,))
+    start_at, shared_at, groups = _groups(group_start, shared_lens, cache)
+    ws, wsb = _workspace(workspace, cache, attn_decode_shared_workspace_bytes, B, max_len, H, cache.kv_heads, D, window,
+                         sinks, groups, max_shared)
+    try:
+        call = _shared_call(*qa, cache._address, table, cols, 0, lens, B, B, 1, max_len, window, *oa, ws, wsb,
+                            cache._stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale,
+                            start_at, shared_at, groups, max_shared)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"attn_decode_shared: {e}") from None
+    status = lib().qgemm_attn_decode_shared(call)
+    if status:
+        _check(status, "qgemm_attn_decode_shared")
+    return out
+
+
+def attn_prefill_shared(q, cache: KVCache, block_table, q_start, seq_lens, max_q: int, max_len: int, group_start,
+                        shared_lens, max_shared: int, scale: float | None = None, window: int = 0, sinks: int = 0,
+                        out=None, workspace: Workspace | None = None):
+    """``attn_prefill`` for a batch whose sequences begin with the same tokens, group by group; the groups as in
+    ``attn_decode_shared``. New tokens may be among the shared ones."""
+    shape, dt, out, qa, oa = _queries(q, cache, out)
+    T, H, D = shape
+    table, cols, seqs = _table(block_table, cache)
+    starts = _int32(q_start, "q_start", cache, (seqs + 1,))
+    lens = _int32(seq_lens, "seq_lens", cache, (seqs,))
+    start_at, shared_at, groups = _groups(group_start, shared_lens, cache)
+    ws, wsb = _workspace(workspace, cache, attn_prefill_shared_workspace_bytes, seqs, T, max_q, max_len, H, cache.kv_heads,
+                         D, window, sinks, groups, max_shared)
+    try:
+        call = _shared_call(*qa, cache._address, table, cols, starts, lens, seqs, T, max_q, max_len, window, *oa, ws, wsb,
+                            cache._stream(cache._index), H, dt, sinks, 1.0 / math.sqrt(D) if scale is None else scale,
+                            start_at, shared_at, groups, max_shared)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"attn_prefill_shared: {e}") from None
+    status = lib().qgemm_attn_prefill_shared(call)
+    if status:
+        _check(status, "qgemm_attn_prefill_shared")
     return out

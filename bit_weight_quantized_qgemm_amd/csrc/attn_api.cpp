@@ -22,6 +22,7 @@ constexpr int kMaxGroup = 128;
 constexpr int64_t kMaxTokenStride = int64_t(1) << 25;
 
 std::atomic<int> g_force_splits{0};
+constexpr int kDecodeStep = 2 * qg::kDecodeWaves;   // token blocks: a pair for each wave
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -157,7 +158,7 @@ qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_
   pl.part_rows = std::min(group, qg::kDecodeRows);
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
   const int64_t blocks = visible_blocks(max_len, 1, mask);
-  constexpr int kStep = 2 * qg::kDecodeWaves;   // one pair of blocks for each wave
+  constexpr int kStep = kDecodeStep;
   const int64_t steps = (blocks + kStep - 1) / kStep;
   // Parts of a tile, by tiles per compute unit and steps (128 tokens) of the longest
   // context. Joining costs about 3 us, a step of a lone workgroup 1.6. Measured on 8
@@ -191,6 +192,44 @@ qg::AttnPlan decode_plan(int64_t num_seqs, int64_t max_len, int q_heads, int kv_
   return pl;
 }
 
+// Token blocks of a tile of K and V of the many-token kernel.
+int prefill_step(int head_dim) { return head_dim <= 128 ? 4 : 2; }
+
+// Tiles of K and V hold 64 tokens (32 for heads above 128 values). One takes a
+// workgroup that has a compute unit for itself 1.25 us, and w of them that share a
+// unit 1.15 w us together (0.9 and 0.65 w for heads of 64); a join of s parts, x MB,
+// costs 2 + 0.08 s + 2.8 sqrt(x) us (16 parts are read at a time), with 0.45 x beyond
+// 40 MB, where the parts leave the caches. A split has to win 5 %. Of 197 shapes
+// (1..512 new tokens on 600..200000, 64 to 256 values, 1..16 sequences) the split
+// that this finds is on average 2 % slower than the best of 1..256 parts (50 tokens
+// on 20000, 64/8 heads: 58 us, best 54, unsplit 329; 12 x 40 on 12000, 32/8 heads of
+// 64, e4m3: 99, best 95, unsplit 174). Where a good part of the context is new, the
+// row tiles see less of it the earlier they stand, and fill the units in whatever
+// order they end: then the mean work counts, and the longest tile (4096 new tokens,
+// 20/20 heads of 80, 640 row tiles: 95 us, in two parts 122).
+// mean: of a row tile's visible part, in the whole.
+int prefill_parts(int64_t row_tiles, int part_rows, int64_t blocks, int head_dim, bool even, double mean) {
+  const int kStep = prefill_step(head_dim);
+  const int cus = qg::device_cu_count();
+  int best = 1;
+  if (row_tiles > 4 * cus) return best;
+  const int steps = (int)((blocks + kStep - 1) / kStep), tiles = (int)row_tiles;
+  const double part_mb = (double)tiles * part_rows * head_dim * 4e-6;
+  const double alone = head_dim <= 64 ? 0.9 : 1.25, shared = head_dim <= 64 ? 0.65 : 1.15;
+  double least = 0;
+  for (int s = 1; s <= steps && s * tiles <= 8 * cus && s <= 2 * cus; s += s < 32 ? 1 : 16) {
+    const int turns = (steps + s - 1) / s, on_unit = (tiles * s + cus - 1) / cus;
+    const double mb = part_mb * s, join = s == 1 ? 0 : 2 + 0.08 * s + std::max(2.8 * std::sqrt(mb), 0.45 * mb);
+    const double work = even ? shared * on_unit : shared * mean * tiles * s / cus;
+    const double cost = turns * (on_unit == 1 ? alone : std::max(alone, work)) + join;
+    if (s == 1 || cost < least * (best == 1 ? 0.95 : 1)) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
 qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int q_heads, int kv_heads, int head_dim,
                           const Mask& mask) {
   qg::AttnPlan pl;
@@ -199,40 +238,71 @@ qg::AttnPlan prefill_plan(int64_t num_seqs, int64_t max_q, int64_t max_len, int 
   pl.part_rows = (int)std::min<int64_t>(rows, qg::kPrefillRows);
   pl.tiles = num_seqs * kv_heads * pl.row_tiles;
   const int64_t blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), mask);
-  // Tiles of K and V hold 64 tokens (32 for heads above 128 values). One takes a
-  // workgroup that has a compute unit for itself 1.25 us, and w of them that share a
-  // unit 1.15 w us together (0.9 and 0.65 w for heads of 64); a join of s parts, x MB,
-  // costs 2 + 0.08 s + 2.8 sqrt(x) us (16 parts are read at a time), with 0.45 x beyond
-  // 40 MB, where the parts leave the caches. A split has to win 5 %. Of 197 shapes
-  // (1..512 new tokens on 600..200000, 64 to 256 values, 1..16 sequences) the split
-  // that this finds is on average 2 % slower than the best of 1..256 parts (50 tokens
-  // on 20000, 64/8 heads: 58 us, best 54, unsplit 329; 12 x 40 on 12000, 32/8 heads of
-  // 64, e4m3: 99, best 95, unsplit 174). Where a good part of the context is new, the
-  // row tiles see less of it the earlier they stand, and fill the units in whatever
-  // order they end: then the mean work counts, and the longest tile (4096 new tokens,
-  // 20/20 heads of 80, 640 row tiles: 95 us, in two parts 122).
-  const int kStep = head_dim <= 128 ? 4 : 2;   // blocks of a tile of K and V
-  const int cus = qg::device_cu_count();
-  int best = 1;
-  if (pl.tiles <= 4 * cus) {
-    const int steps = (int)((blocks + kStep - 1) / kStep), tiles = (int)pl.tiles;
-    const double part_mb = (double)tiles * pl.part_rows * head_dim * 4e-6;
-    const double alone = head_dim <= 64 ? 0.9 : 1.25, shared = head_dim <= 64 ? 0.65 : 1.15;
-    const bool even = mask.window != 0 || max_q * 5 < max_len;
-    const double mean = even ? 1 : 1 - 0.5 * std::min(max_q, max_len) / (double)max_len;   // of a tile's visible part
-    double least = 0;
-    for (int s = 1; s <= steps && s * tiles <= 8 * cus && s <= 2 * cus; s += s < 32 ? 1 : 16) {
-      const int turns = (steps + s - 1) / s, on_unit = (tiles * s + cus - 1) / cus;
-      const double mb = part_mb * s, join = s == 1 ? 0 : 2 + 0.08 * s + std::max(2.8 * std::sqrt(mb), 0.45 * mb);
-      const double work = even ? shared * on_unit : shared * mean * tiles * s / cus;
-      const double cost = turns * (on_unit == 1 ? alone : std::max(alone, work)) + join;
-      if (s == 1 || cost < least * (best == 1 ? 0.95 : 1)) {
-        least = cost;
-        best = s;
-      }
-    }
+  const bool even = mask.window != 0 || max_q * 5 < max_len;
+  const double mean = even ? 1 : 1 - 0.5 * std::min(max_q, max_len) / (double)max_len;
+  split(pl, blocks, prefill_parts(pl.tiles, pl.part_rows, blocks, head_dim, even, mean), prefill_step(head_dim), head_dim);
+  return pl;
+}
+
+// The groups of a batch whose sequences share tokens.
+struct Sharing {
+  const int32_t* group_start;
+  const int32_t* shared_lens;
+  int64_t num_groups, max_shared;
+};
+std::atomic<int> g_force_sharing{0};   // 1: always, 2: never
+
+// Whether the shared tokens are computed apart.
+bool worth_sharing(int64_t num_seqs, int64_t num_groups, int64_t max_shared) {
+  const int force = g_force_sharing.load();
+  if (num_groups == 0 || max_shared < qg::kTokBlock || force == 2) return false;
+  return force == 1 || num_seqs >= 2 * num_groups;
+}
+
+// Sums of rows over shared tokens, next to those over own ones. Tiles of 128 rows are counted
+// as if the groups held them all and each began a tile (attn_shared.h).
+qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, int64_t max_len, int q_heads,
+                           int kv_heads, int head_dim, const Mask& mask, int64_t num_groups, int64_t max_shared,
+                           bool prefill) {
+  qg::SharedPlan pl;
+  max_shared = std::min(max_shared, max_len) / qg::kTokBlock * qg::kTokBlock;
+  const int64_t rows = num_tokens * (q_heads / kv_heads);
+  pl.tiles = (rows / qg::kPrefillRows + num_groups) * kv_heads;
+  const int64_t row_tiles = (max_q * (q_heads / kv_heads) + qg::kPrefillRows - 1) / qg::kPrefillRows;
+  // (the join's grid has up to 32 workgroups per row tile)
+  pl.share = worth_sharing(num_seqs, num_groups, max_shared) && pl.tiles <= (INT32_MAX >> 10) &&
+             num_seqs * kv_heads * row_tiles <= INT32_MAX / 32;
+  if (!pl.share) {
+    pl.own = prefill ? prefill_plan(num_seqs, max_q, max_len, q_heads, kv_heads, head_dim, mask)
+                     : decode_plan(num_seqs, max_len, q_heads, kv_heads, head_dim, mask);
+    pl.ws_bytes = pl.own.ws_bytes;
+    return pl;
   }
-  split(pl, blocks, best, kStep, head_dim);
+  // Own tokens: as many as the longest context has past the longest shared run, as a guess;
+  // the kernel cuts each sequence's own tokens into that many parts at most.
+  const int64_t own_len = std::max({max_len - max_shared, max_q, int64_t(1)});
+  const Mask own_mask = bounded_mask(own_len, mask.window, mask.sinks);
+  pl.own = prefill ? prefill_plan(num_seqs, max_q, own_len, q_heads, kv_heads, head_dim, own_mask)
+                   : decode_plan(num_seqs, own_len, q_heads, kv_heads, head_dim, own_mask);
+  const int64_t blocks = max_shared / qg::kTokBlock;
+  const int64_t live = std::max(num_groups, (rows + qg::kPrefillRows - 1) / qg::kPrefillRows) * kv_heads;
+  const int force = g_force_splits.load(), step = prefill_step(head_dim);
+  const int64_t parts =
+      force ? force : prefill_parts(live, (int)std::min<int64_t>(rows, qg::kPrefillRows), blocks, head_dim, true, 1);
+  const int64_t per = (blocks + parts - 1) / parts;
+  pl.split_blocks = (int)((per + step - 1) / step * step);
+  pl.splits = (int)((blocks + pl.split_blocks - 1) / pl.split_blocks);
+  size_t end = qg::kCounterBytes;
+  if (pl.own.splits > 1 || prefill) {
+    const size_t own_parts = (size_t)pl.own.tiles * pl.own.splits;
+    pl.own.stats_offset = end;
+    pl.own.partial_offset = end + qg::align256(own_parts * pl.own.part_rows * 8);
+    end = pl.own.partial_offset + qg::align256(own_parts * pl.own.part_rows * head_dim * 4);
+  }
+  const size_t shared_rows = (size_t)pl.tiles * pl.splits * qg::kPrefillRows;
+  pl.stats_offset = end;
+  pl.partial_offset = end + shared_rows * 8;
+  pl.ws_bytes = pl.partial_offset + shared_rows * head_dim * 4;
   return pl;
 }
 
@@ -246,7 +316,13 @@ int check_attn_shape(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t
   return check_heads(q_heads, kv_heads);
 }
 
-int run_attn(const qgemm_attn_call& g, bool prefill) {
+int check_groups(int64_t num_groups, int64_t max_shared) {
+  if (num_groups < 0 || num_groups > kMaxSeqs || max_shared < 0) return QGEMM_ERR_SHAPE;
+  return QGEMM_OK;
+}
+
+// sharing: NULL for a call without shared tokens.
+int run_attn(const qgemm_attn_call& g, bool prefill, const Sharing* sharing) {
   const qgemm_kv_cache* c = g.cache;
   const int64_t num_tokens = prefill ? g.num_tokens : g.num_seqs, max_q = prefill ? g.max_q : 1;
   const int32_t* q_start = prefill ? g.q_start : nullptr;
@@ -255,6 +331,10 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
   int st = check_attn_shape(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, g.window, g.sinks);
   if (st) return st;
   if (num_tokens < 0 || num_tokens > kMaxTokens || max_q < 0 || max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
+  if (sharing) {
+    st = check_groups(sharing->num_groups, sharing->max_shared);
+    if (st) return st;
+  }
   st = check_cache(c, g.act_dtype);
   if (st) return st;
   if (!positive(g.scale) || !positive(g.scale * c->k_scale)) return QGEMM_ERR_RANGE;
@@ -271,13 +351,25 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
     return QGEMM_ERR_SHAPE;
 
   const Mask mask = bounded_mask(g.max_len, g.window, g.sinks);
-  const qg::AttnPlan pl = prefill
-                              ? prefill_plan(g.num_seqs, max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask)
-                              : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask);
+  qg::SharedPlan sp;
+  if (sharing) {
+    if (sharing->num_groups > 0) {
+      if (!sharing->group_start || !sharing->shared_lens) return QGEMM_ERR_NULL;
+      if (!aligned(sharing->group_start, 4) || !aligned(sharing->shared_lens, 4)) return QGEMM_ERR_ALIGN;
+    }
+    sp = shared_plan(g.num_seqs, num_tokens, max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask,
+                     sharing->num_groups, sharing->max_shared, prefill);
+  } else {
+    sp.own = prefill ? prefill_plan(g.num_seqs, max_q, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask)
+                     : decode_plan(g.num_seqs, g.max_len, g.q_heads, c->kv_heads, c->head_dim, mask);
+    sp.ws_bytes = sp.own.ws_bytes;
+  }
+  const qg::AttnPlan& pl = sp.own;
+  const size_t ws_bytes = sp.ws_bytes;
   if (pl.tiles * pl.splits > INT32_MAX) return QGEMM_ERR_SHAPE;
-  if (pl.ws_bytes > 0) {
+  if (ws_bytes > 0) {
     if (!g.workspace) return QGEMM_ERR_NULL;
-    if (g.workspace_bytes < pl.ws_bytes) return QGEMM_ERR_WORKSPACE;
+    if (g.workspace_bytes < ws_bytes) return QGEMM_ERR_WORKSPACE;
     if (!aligned(g.workspace, 16)) return QGEMM_ERR_ALIGN;
   }
   const Extent out = extent3(g.out, num_tokens, g.out_token_stride, g.q_heads, g.out_head_stride, c->head_dim);
@@ -287,16 +379,16 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
                            extent(g.block_table, g.num_seqs * g.table_stride, 4),
                            extent(g.seq_lens, g.num_seqs, 4),
                            extent(q_start, g.num_seqs + 1, 4),
-                           extent(pl.ws_bytes ? g.workspace : nullptr, (int64_t)pl.ws_bytes, 1)};
+                           extent(sharing ? sharing->group_start : nullptr, sharing ? sharing->num_groups + 1 : 0, 4),
+                           extent(sharing ? sharing->shared_lens : nullptr, sharing ? sharing->num_groups : 0, 4)};
+  const Extent ws = extent(ws_bytes ? g.workspace : nullptr, (int64_t)ws_bytes, 1);
   for (const Extent& e : others)
-    if (overlap(out, e)) return QGEMM_ERR_ALIAS;
-  if (pl.ws_bytes)
-    for (const Extent& e : others)
-      if (&e != &others[6] && overlap(others[6], e)) return QGEMM_ERR_ALIAS;
+    if (overlap(out, e) || overlap(ws, e)) return QGEMM_ERR_ALIAS;
+  if (overlap(out, ws)) return QGEMM_ERR_ALIAS;
   st = qg::check_current_device();
   if (st) return st;
 
-  qg::AttnArgs a{};
+  qg::SharedArgs a{};
   a.q = g.q;
   a.out = g.out;
   a.q_ts = g.q_token_stride;
@@ -326,16 +418,35 @@ int run_attn(const qgemm_attn_call& g, bool prefill) {
   a.inv_tiles = 1.0 / (double)pl.tiles;
   a.scale_log2 = g.scale * c->k_scale * 1.44269504088896340736f;
   a.v_scale = c->v_scale;
-  if (pl.ws_bytes) {
-    char* ws = static_cast<char*>(g.workspace);
-    a.counters = reinterpret_cast<uint32_t*>(ws);
-    a.stats = reinterpret_cast<float*>(ws + pl.stats_offset);
-    a.partial = reinterpret_cast<float*>(ws + pl.partial_offset);
+  if (ws_bytes) {
+    char* base = static_cast<char*>(g.workspace);
+    a.counters = reinterpret_cast<uint32_t*>(base);
+    a.stats = reinterpret_cast<float*>(base + pl.stats_offset);
+    a.partial = reinterpret_cast<float*>(base + pl.partial_offset);
+    a.shared_stats = reinterpret_cast<float*>(base + sp.stats_offset);
+    a.shared_partial = reinterpret_cast<float*>(base + sp.partial_offset);
   }
   const bool bf16 = g.act_dtype == QGEMM_DT_BF16, fp8 = c->dtype == QGEMM_DT_FP8;
   hipStream_t s = static_cast<hipStream_t>(g.stream);
-  const hipError_t e = prefill ? qg::launch_attn_prefill(a, bf16, fp8, pl.tiles, s)
-                               : qg::launch_attn_decode(a, bf16, fp8, pl.tiles, s);
+  hipError_t e;
+  if (sp.share) {
+    a.group_start = sharing->group_start;
+    a.shared_lens = sharing->shared_lens;
+    a.num_groups = (int32_t)sharing->num_groups;
+    a.max_shared = (int32_t)std::min(sharing->max_shared, g.max_len);
+    a.shared_tiles = (int32_t)sp.tiles;
+    a.shared_splits = sp.splits;
+    a.shared_split_blocks = sp.split_blocks;
+    a.split_step = prefill ? prefill_step(c->head_dim) : kDecodeStep;
+    a.inv_shared_tiles = 1.0 / (double)sp.tiles;
+    e = qg::launch_attn_shared(a, bf16, fp8, s);
+    if (e == hipSuccess)
+      e = prefill ? qg::launch_attn_prefill_own(a, bf16, fp8, pl.tiles, s)
+                  : qg::launch_attn_decode_own(a, bf16, fp8, pl.tiles, s);
+  } else {
+    e = prefill ? qg::launch_attn_prefill(a, bf16, fp8, pl.tiles, s)
+                : qg::launch_attn_decode(a, bf16, fp8, pl.tiles, s);
+  }
   if (e != hipSuccess) return qg::fail_hip(e, "kernel launch");
   return QGEMM_OK;
 }
@@ -486,7 +597,7 @@ int qgemm_attn_decode_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t
 }
 
 int qgemm_attn_decode_call(const qgemm_attn_call* call) {
-  return call ? run_attn(*call, false) : QGEMM_ERR_NULL;
+  return call ? run_attn(*call, false, nullptr) : QGEMM_ERR_NULL;
 }
 
 int qgemm_attn_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, const qgemm_kv_cache* cache,
@@ -515,7 +626,7 @@ int qgemm_attn_decode(const void* q, int64_t q_token_stride, int64_t q_head_stri
   g.act_dtype = act_dtype;
   g.sinks = sinks;
   g.scale = scale;
-  return run_attn(g, false);
+  return run_attn(g, false, nullptr);
 }
 
 int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t max_len, int32_t q_heads,
@@ -533,7 +644,7 @@ int qgemm_attn_prefill_workspace_bytes(int64_t num_seqs, int64_t max_q, int64_t 
 }
 
 int qgemm_attn_prefill_call(const qgemm_attn_call* call) {
-  return call ? run_attn(*call, true) : QGEMM_ERR_NULL;
+  return call ? run_attn(*call, true, nullptr) : QGEMM_ERR_NULL;
 }
 
 int qgemm_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const qgemm_kv_cache* cache,
@@ -566,7 +677,57 @@ int qgemm_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   g.act_dtype = act_dtype;
   g.sinks = sinks;
   g.scale = scale;
-  return run_attn(g, true);
+  return run_attn(g, true, nullptr);
+}
+
+int qgemm_attn_decode_shared_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t q_heads, int32_t kv_heads,
+                                             int32_t head_dim, int64_t window, int32_t sinks, int64_t num_groups,
+                                             int64_t max_shared, size_t* bytes) {
+  if (!bytes) return QGEMM_ERR_NULL;
+  int st = check_attn_shape(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks);
+  if (!st) st = check_groups(num_groups, max_shared);
+  if (st) return st;
+  const Mask mask = bounded_mask(max_len, window, sinks);
+  *bytes = num_seqs == 0 ? 0
+                         : shared_plan(num_seqs, num_seqs, 1, max_len, q_heads, kv_heads, head_dim, mask, num_groups,
+                                       max_shared, false)
+                               .ws_bytes;
+  return QGEMM_OK;
+}
+
+int qgemm_attn_prefill_shared_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int64_t max_q, int64_t max_len,
+                                              int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t window,
+                                              int32_t sinks, int64_t num_groups, int64_t max_shared, size_t* bytes) {
+  if (!bytes) return QGEMM_ERR_NULL;
+  int st = check_attn_shape(num_seqs, max_len, q_heads, kv_heads, head_dim, window, sinks);
+  if (!st) st = check_groups(num_groups, max_shared);
+  if (st) return st;
+  if (num_tokens < 0 || num_tokens > kMaxTokens || max_q < 0 || max_q > kMaxTokens) return QGEMM_ERR_SHAPE;
+  const Mask mask = bounded_mask(max_len, window, sinks);
+  *bytes = num_seqs == 0 || num_tokens == 0 || max_q == 0
+               ? 0
+               : shared_plan(num_seqs, num_tokens, max_q, max_len, q_heads, kv_heads, head_dim, mask, num_groups,
+                             max_shared, true)
+                     .ws_bytes;
+  return QGEMM_OK;
+}
+
+int qgemm_attn_decode_shared(const qgemm_attn_shared_call* call) {
+  if (!call) return QGEMM_ERR_NULL;
+  const Sharing sharing{call->group_start, call->shared_lens, call->num_groups, call->max_shared};
+  return run_attn(call->attn, false, &sharing);
+}
+
+int qgemm_attn_prefill_shared(const qgemm_attn_shared_call* call) {
+  if (!call) return QGEMM_ERR_NULL;
+  const Sharing sharing{call->group_start, call->shared_lens, call->num_groups, call->max_shared};
+  return run_attn(call->attn, true, &sharing);
+}
+
+int qgemm_attn_set_sharing(int mode) {
+  if (mode < 0 || mode > 2) return QGEMM_ERR_RANGE;
+  g_force_sharing.store(mode);
+  return QGEMM_OK;
 }
 
 int qgemm_attn_set_splits(int splits) {

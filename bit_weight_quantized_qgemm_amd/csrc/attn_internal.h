@@ -70,6 +70,21 @@ struct AttnArgs {
   uint32_t first_block;     // number of the launch's first workgroup
 };
 
+// The same for a batch whose sequences share their first tokens group by group:
+// sequences group_start[g]..group_start[g+1]-1 the first shared_lens[g] ones.
+struct SharedArgs : AttnArgs {
+  const int32_t* group_start;
+  const int32_t* shared_lens;
+  float* shared_partial;    // [shared tile][shared split][kPrefillRows][head_dim]
+  float* shared_stats;      // [shared tile][shared split][kPrefillRows] (maximum, sum)
+  int32_t num_groups, max_shared;
+  int32_t shared_tiles;     // tiles of 128 rows of a group and key-value head
+  int32_t shared_splits;
+  int32_t shared_split_blocks;
+  int32_t split_step;       // token blocks of an own part: a multiple of this
+  double inv_shared_tiles;
+};
+
 struct AttnPlan {
   int64_t tiles = 0;        // row tiles of the launch
   int row_tiles = 1;        // per (sequence, key-value head)
@@ -100,8 +115,22 @@ struct AppendArgs {
   uint32_t first_block;   // number of the launch's first workgroup
 };
 
+// Workspace of a batch with shared tokens: the own parts', then the shared ones'.
+struct SharedPlan {
+  AttnPlan own;
+  bool share = false;       // false: computed as if nothing were shared
+  int64_t tiles = 0;        // of shared rows
+  int splits = 1;
+  int split_blocks = 1;
+  size_t stats_offset = 0, partial_offset = 0, ws_bytes = 0;
+};
+
 hipError_t launch_append(const AppendArgs& a, bool bf16, bool fp8, bool interleaved, hipStream_t s);
 hipError_t launch_attn_decode(const AttnArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
 hipError_t launch_attn_prefill(const AttnArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
+// The shared tokens of all groups; then each sequence's own ones, joined with them.
+hipError_t launch_attn_shared(const SharedArgs& a, bool bf16, bool fp8, hipStream_t s);
+hipError_t launch_attn_decode_own(const SharedArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
+hipError_t launch_attn_prefill_own(const SharedArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
 
 }  // namespace qg

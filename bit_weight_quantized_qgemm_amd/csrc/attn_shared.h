@@ -1,0 +1,170 @@
+// Device-side helpers of attention over tokens that several sequences share: which group
+// a sequence or a tile of rows belongs to, and the join of what was computed for both kinds
+// of tokens.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_device.h"
+
+namespace qg {
+
+// Number of the entries 0..n-1 that are at most x, for entries that never fall; the same in
+// all lanes of a wave, which looks at 64 of them at a time (two rounds up to 4096). Whatever
+// the entries hold, only those are read and the loop ends: n falls in every turn.
+template <class Entry>
+__device__ __forceinline__ int count_up_to(int n, int x, const Entry& entry) {
+  const int lane = threadIdx.x & 63;
+  int first = 0;
+  while (n > 0) {
+    const int step = (n + 63) / 64, i = lane * step;
+    const int below = __popcll(__ballot(i < n && entry(first + min(i, n - 1)) <= x));
+    if (step == 1 || below == 0) return first + below;
+    const int skip = (below - 1) * step + 1;   // entries known to be at most x
+    first += skip;
+    n = min(step - 1, n - skip);
+  }
+  return first;
+}
+
+__device__ __forceinline__ int bounded_seq(const SharedArgs& p, int seq) { return min(max(seq, 0), p.num_seqs); }
+// Tokens that a group's kernel takes as shared: whole blocks, so that both parts of a
+// context consist of whole ones (the rest is read through each sequence's own entries).
+__device__ __forceinline__ int shared_of(const SharedArgs& p, int group) {
+  return min(max(scalar_load(p.shared_lens + group), 0), p.max_shared) / kTokBlock * kTokBlock;
+}
+// First row of q of sequence seq (tokens are sequences in a call with one token each).
+__device__ __forceinline__ int token_of(const SharedArgs& p, int seq) {
+  return p.q_start ? min(max(p.q_start[seq], 0), p.num_tokens) : seq;
+}
+
+struct SharedGroup {
+  int group, seq;   // its number and first sequence
+  int shared;       // tokens shared (0: no group)
+};
+__device__ __forceinline__ SharedGroup group_of(const SharedArgs& p, int seq) {
+  const int n = count_up_to(p.num_groups + 1, seq, [&](int i) { return p.group_start[i]; });
+  if (n < 1 || n > p.num_groups) return SharedGroup{0, 0, 0};
+  const int first = bounded_seq(p, scalar_load(p.group_start + n - 1));
+  if (first > seq) return SharedGroup{0, 0, 0};   // entries that fall
+  return SharedGroup{n - 1, first, shared_of(p, n - 1)};
+}
+
+// Tiles of 128 rows are numbered without a count of anybody's rows: group g, whose first row
+// is number r of all, begins with tile r / 128 + g. A group of n rows needs at most
+// n / 128 + 1 tiles (rounded down), so the next one's first is past its last.
+struct GroupRows {
+  int seq;                // first sequence
+  int token, token_end;   // rows of q
+  int first_tile;
+  int shared;
+};
+__device__ __forceinline__ GroupRows group_of_tile(const SharedArgs& p, int t) {
+  auto first_tile = [&](int g) { return token_of(p, bounded_seq(p, p.group_start[g])) * p.group / kPrefillRows + g; };
+  const int n = count_up_to(p.num_groups, t, first_tile);
+  if (n < 1) return GroupRows{0, 0, 0, 0, 0};
+  GroupRows r;
+  r.seq = __builtin_amdgcn_readfirstlane(bounded_seq(p, p.group_start[n - 1]));
+  r.token = __builtin_amdgcn_readfirstlane(token_of(p, r.seq));
+  r.token_end = __builtin_amdgcn_readfirstlane(token_of(p, bounded_seq(p, p.group_start[n])));
+  r.first_tile = r.token * p.group / kPrefillRows + n - 1;
+  if (r.seq >= p.num_seqs || r.first_tile > t) r.token_end = r.token;   // entries that fall
+  r.shared = shared_of(p, n - 1);
+  return r;
+}
+
+// Position in its own sequence of row `row` of a group whose first row of q is `token` and first
+// sequence `seq`; -1 for a row that the call does not compute. Whole waves call it, for rows
+// between `first` and `last`.
+__device__ __forceinline__ int position_of(const SharedArgs& p, int seq, int token, int row, int first, int last) {
+  const int mine = token + divide(row, p.inv_group);
+  if (!p.q_start) return min(max(p.lens[mine], 0), p.max_len) - 1;
+  const int from = token + divide_uniform(first, p.inv_group), to = token + divide_uniform(last, p.inv_group);
+  // the sequence of the first row's token, then those that begin up to the last one's
+  int my_seq = seq + count_up_to(p.num_seqs - seq, from, [&](int i) { return p.q_start[seq + 1 + i]; });
+  for (int s = __builtin_amdgcn_readfirstlane(my_seq) + 1; s <= p.num_seqs; s += 64) {
+    const int starts = p.q_start[min(s + (int)(threadIdx.x & 63), p.num_seqs)], n = min(64, p.num_seqs - s + 1);
+    bool more = true;
+    for (int i = 0; i < n && more; ++i) {
+      const int start = __builtin_amdgcn_readlane(starts, i);
+      more = start <= to;
+      my_seq += more && start <= mine;
+    }
+    if (!more) break;
+  }
+  if (my_seq >= p.num_seqs) return -1;
+  const int q0 = token_of(p, my_seq), q1 = token_of(p, my_seq + 1);
+  const int rows = min(max(q1 - q0, 0), p.max_q), i = mine - q0;
+  const int len = min(max(p.lens[my_seq], 0), p.max_len);
+  return i >= 0 && i < rows ? len - rows + i : -1;
+}
+
+// A sequence's virtual blocks past the tokens that it shares, in at most `splits` parts of
+// whole steps.
+struct OwnBlocks {
+  int first, split_blocks, parts;
+};
+__device__ __forceinline__ OwnBlocks own_blocks(const Visible& see, int shared, int splits, int step) {
+  const int block = shared / kTokBlock;
+  OwnBlocks o;
+  o.first = block <= see.sink_blocks ? block : max(see.sink_blocks, block - see.skip);
+  const int blocks = max(0, see.blocks - o.first);
+  const int each = (blocks + splits - 1) / splits;
+  o.split_blocks = max(step, (each + step - 1) / step * step);
+  o.parts = max(1, (blocks + o.split_blocks - 1) / o.split_blocks);
+  return o;
+}
+
+// Four outputs of a row before the division: reference maximum, sum of weights, sums.
+struct RowSums {
+  float m = kNegInf, total = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+};
+// Adds `parts` parts to them, in order; load(s, y, m, l) gives the four sums, the maximum and
+// the sum of weights of part s.
+template <class Load>
+__device__ __forceinline__ void add_parts(RowSums& r, int parts, const Load& load) {
+  constexpr int kBatch = 8;   // parts whose loads are in flight together
+  for (int s0 = 0; s0 < parts; s0 += kBatch) {
+    f32x4 y[kBatch];
+    float ym[kBatch], yl[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) load(min(s0 + u, parts - 1), y[u], ym[u], yl[u]);
+    float top = r.m;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ym[u]);   // re-read last parts change nothing
+    const float base = top == kNegInf ? 0.f : top;
+    const float f0 = exp2_of(r.m - base);
+    r.total *= f0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.o[i] *= f0;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (s0 + u < parts) {
+        const float f = exp2_of(ym[u] - base);
+        r.total += f * yl[u];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.o[i] += f * y[u][i];
+      }
+    }
+    r.m = top;
+  }
+}
+// Adds the shared part of a row: head `head` of the key-value head's group, of token `token`
+// of the sequences' group; values d..d+3.
+__device__ __forceinline__ void add_shared_parts(RowSums& r, const SharedArgs& p, const SharedGroup& g, int kv_head,
+                                                 int token, int head, int d) {
+  const int parts = (g.shared / kTokBlock + p.shared_split_blocks - 1) / p.shared_split_blocks;
+  const int row = max(0, token) * p.group + head;
+  const int t = token_of(p, g.seq) * p.group / kPrefillRows + g.group + row / kPrefillRows;
+  const int64_t first = ((int64_t)t * p.kv_heads + kv_head) * p.shared_splits * kPrefillRows + row % kPrefillRows;
+  add_parts(r, parts, [&](int s, f32x4& y, float& m, float& l) {
+    const int64_t at = first + s * kPrefillRows;
+    y = *reinterpret_cast<const f32x4*>(p.shared_partial + at * p.head_dim + d);
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(p.shared_stats + 2 * at);
+    m = ml[0];
+    l = ml[1];
+  });
+}
+
+}  // namespace qg

@@ -498,6 +498,48 @@ int qgemm_attn_decode_call(const qgemm_attn_call* call);
 int qgemm_attn_prefill_call(const qgemm_attn_call* call);
 
 /*
+ * The two attention calls for a batch whose sequences begin with the same tokens, group by
+ * group: sequences group_start[g] .. group_start[g+1]-1 (int32 [num_groups + 1] in device
+ * memory, nondecreasing) have the first shared_lens[g] tokens (int32 [num_groups], device
+ * memory) in the same pages, which each of their table rows names. Sequences before the first
+ * group and after the last are in none. The results are those of qgemm_attn_decode and
+ * qgemm_attn_prefill for the same arguments, to their accuracy; keys and values of shared
+ * tokens are read and computed once for all rows of a group, 128 at a time, and the parts of a
+ * row joined in order. Any shared_lens is right for which the pages are the same (0, one past
+ * a sequence's end); those above max_shared are taken as max_shared (a host number, which
+ * sizes grid and workspace), and up to 15 tokens of one, whose block is not whole, are read
+ * for each sequence apart.
+ *   - Keys and values of the tokens below shared_lens[g] have to be finite, seen or not.
+ *   - The weights of shared tokens are rounded to one 16-bit term, as in prefill.
+ *   - num_groups is 0..65535. Where the batch has less than two sequences per group the call
+ *     is computed as if nothing were shared.
+ * The struct is read before the call returns; attn holds what the plain call takes.
+ */
+typedef struct qgemm_attn_shared_call {
+  qgemm_attn_call attn;
+  const int32_t* group_start;
+  const int32_t* shared_lens;
+  int64_t num_groups, max_shared;
+} qgemm_attn_shared_call;
+
+int qgemm_attn_decode_shared_workspace_bytes(int64_t num_seqs, int64_t max_len, int32_t q_heads,
+                                             int32_t kv_heads, int32_t head_dim, int64_t window,
+                                             int32_t sinks, int64_t num_groups, int64_t max_shared,
+                                             size_t* bytes);
+int qgemm_attn_decode_shared(const qgemm_attn_shared_call* call);
+int qgemm_attn_prefill_shared_workspace_bytes(int64_t num_seqs, int64_t num_tokens, int64_t max_q,
+                                              int64_t max_len, int32_t q_heads, int32_t kv_heads,
+                                              int32_t head_dim, int64_t window, int32_t sinks,
+                                              int64_t num_groups, int64_t max_shared, size_t* bytes);
+int qgemm_attn_prefill_shared(const qgemm_attn_shared_call* call);
+
+/*
+ * Whether later calls of the two above compute shared tokens apart: 0 where that is worth it,
+ * 1 always, 2 never. For tests and tuning; affects their workspace queries too.
+ */
+int qgemm_attn_set_sharing(int mode);
+
+/*
  * Force the number of parts into which later attention calls of this process
  * split the cache's length (1..1024; 0: automatic). For tests and tuning, like
  * qgemm_set_plan_override; affects the attention workspace queries too.
