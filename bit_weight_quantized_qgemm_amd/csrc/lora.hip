@@ -96,31 +96,33 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan(LoraPlanArgs p) {
 struct LoraTile {
   int adapter, first, rows, rank;
 };
-__device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int tile) {
-  const int32_t* at = p.plan + p.tiles_at + 4 * tile;
+__device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int tile, int tiles_at, int count_at) {
+  const int32_t* at = p.plan + tiles_at + 4 * tile;
   LoraTile t{scalar_load(at), scalar_load(at + 1), scalar_load(at + 2), p.rank};
   // a plan of other numbers of rows and adapters is not followed
   const bool fits = scalar_load(p.plan) == p.tokens && scalar_load(p.plan + 1) == p.adapters;
-  if (!fits || tile >= scalar_load(p.plan + (p.wide ? 3 : 2))) t.rows = 0;
+  if (!fits || tile >= scalar_load(p.plan + count_at)) t.rows = 0;
   if (t.rows > 0 && t.adapter >= 0 && p.ranks)
     t.rank = (min(max(scalar_load(p.ranks + t.adapter), 0), p.rank) + 7) / 8 * 8;
   return t;
 }
 
-// y[row][16 i ..] += A x over a part of K: RB * 16 rows by NT * 16 ranks of one adapter.
-// The four waves take a quarter of the part each and meet in LDS. Ranks are the rows of
-// the product (first operand) and tokens its columns, so that a lane ends with four ranks
-// of one token; both operands go from memory to registers as they stand. Rows and ranks
-// that do not exist repeat the last one's loads and are dropped at the end.
+// y = A x: RB * 16 rows by NT * 16 ranks of one adapter, over a part of K. The four waves
+// take a quarter of the part each and meet in LDS; the last workgroup of a tile to arrive
+// adds the parts, in order. Ranks are the rows of the product (first operand) and tokens
+// its columns, so that a lane ends with four ranks of one token; both operands go from
+// memory to registers as they stand. Rows and ranks that do not exist repeat the last
+// one's loads and are dropped at the end.
 template <class F, int RB, int NT>
 __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
-  constexpr int kUnroll = RB == 1 ? (NT == 1 ? 8 : 4) : 2;
+    constexpr int kUnroll = RB == 1 ? 4 : 2;
   __shared__ __attribute__((aligned(16))) float part[kLoraWaves][RB * NT][64][4];
+  __shared__ int flag;
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile_no = blockIdx.x % (uint32_t)p.cap, rest = blockIdx.x / (uint32_t)p.cap;
-  const int chunk = rest % p.chunks, split = rest / p.chunks;
-  const LoraTile t = lora_tile(p, tile_no);
+  const int parts = p.chunks * p.splits, tile_no = blockIdx.x / (uint32_t)parts, rest = blockIdx.x - tile_no * parts;
+  const int split = rest / p.chunks, chunk = rest - split * p.chunks;
+  const LoraTile t = RB == 1 ? lora_tile(p, tile_no, p.tiles16, 2) : lora_tile(p, tile_no, p.tiles64, 3);
   if (t.rows <= 0 || t.adapter < 0) return;
   using T = typename F::T;
   const int tiles = p.slices * p.rank_tiles;
@@ -147,31 +149,42 @@ __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int begin = split * p.split_k + wave * (p.split_k / kLoraWaves);
-  const int end = min(begin + p.split_k / kLoraWaves, p.k);
-  int k = begin + 8 * h;
-  auto steps = [&](auto count) {
-    constexpr int n = decltype(count)::value;
-    u32x4 xr[n][RB], ar[n][NT];
+  const int begin = split * p.split_k, end = min(begin + p.split_k, p.k);
+  // Runs of kUnroll steps go to the waves in turn, so that a workgroup reads rows in long
+  // stretches; one run's loads stand in flight beside the products of the one before.
+  struct Steps {
+    u32x4 x[kUnroll][RB], a[kUnroll][NT];
+  };
+  auto load = [&](Steps& o, int run) {
+    const int k = begin + run * (32 * kUnroll) + 8 * h;
 #pragma unroll
-    for (int s = 0; s < n; ++s) {
+    for (int s = 0; s < kUnroll; ++s) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) ar[s][i] = *reinterpret_cast<const u32x4*>(ap[i] + k + 32 * s);
+      for (int i = 0; i < NT; ++i) o.a[s][i] = *reinterpret_cast<const u32x4*>(ap[i] + k + 32 * s);
 #pragma unroll
-      for (int b = 0; b < RB; ++b) xr[s][b] = *reinterpret_cast<const u32x4*>(xp[b] + k + 32 * s);
+      for (int b = 0; b < RB; ++b) o.x[s][b] = *reinterpret_cast<const u32x4*>(xp[b] + k + 32 * s);
     }
+  };
+  auto multiply = [&](const Steps& o) {
 #pragma unroll
-    for (int s = 0; s < n; ++s)
+    for (int s = 0; s < kUnroll; ++s)
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int b = 0; b < RB; ++b) acc[b][i] = F::mfma16(ar[s][i], xr[s][b], acc[b][i]);
-    k += 32 * n;
+        for (int b = 0; b < RB; ++b) acc[b][i] = F::mfma16(o.a[s][i], o.x[s][b], acc[b][i]);
   };
-  int left = (end - begin) / 32;   // may be negative
-  for (; left >= kUnroll; left -= kUnroll) steps(std::integral_constant<int, kUnroll>{});
-  for (; left > 0; --left) steps(std::integral_constant<int, 1>{});
-  if (end > begin && (end - begin) % 32 != 0) {   // the end of K, no whole step
+  const int runs = (end - begin) / (32 * kUnroll);
+  Steps even, odd;
+  if (wave < runs) load(even, wave);
+  for (int r = wave; r < runs; r += 2 * kLoraWaves) {
+    if (r + kLoraWaves < runs) load(odd, r + kLoraWaves);
+    multiply(even);
+    if (r + 2 * kLoraWaves < runs) load(even, r + 2 * kLoraWaves);
+    if (r + kLoraWaves < runs) multiply(odd);
+  }
+  // what is left, step by step; the end of K may be within one
+  for (int k0 = begin + (runs * kUnroll + wave) * 32; k0 < end; k0 += kLoraWaves * 32) {
+    const int k = k0 + 8 * h;
     const bool there = k < end;
     u32x4 xr[RB], ar[NT];
 #pragma unroll
@@ -195,156 +208,227 @@ __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(part[wave][b * NT + i][lane]) = acc[b][i];
   __syncthreads();
-  for (int x = wave; x < RB * NT; x += kLoraWaves) {
-    f32x4 y = *reinterpret_cast<const f32x4*>(part[0][x][lane]);
-#pragma unroll
-    for (int w = 1; w < kLoraWaves; ++w) {
-      const f32x4 z = *reinterpret_cast<const f32x4*>(part[w][x][lane]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += z[i];
-    }
+  constexpr uint32_t kPartBytes = RB * NT * 64 * 16;
+  const int64_t first_part = ((int64_t)tile_no * p.chunks + chunk) * p.splits;
+  const rsrc_t mine = make_rsrc(p.partial + (first_part + split) * (kPartBytes / 4), kPartBytes);
+  auto finish_tile = [&](int x, f32x4 y) {
     const int at = chunk * NT + x % NT, row = x / NT * 16 + c, r0 = at % p.rank_tiles * 16 + 4 * h;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (r0 + i >= t.rank) y[i] = 0.f;
     if (at < tiles && row < t.rows)
-      *reinterpret_cast<f32x4*>(p.partial + (((int64_t)split * p.tokens + t.first + row) * tiles + at) * 16 + 4 * h) = y;
+      *reinterpret_cast<f32x4*>(p.y + ((int64_t)(t.first + row) * tiles + at) * 16 + 4 * h) = y;
+  };
+#pragma unroll
+  for (int n = 0; n < (RB * NT + 3) / 4; ++n) {
+    const int x = n * kLoraWaves + wave;
+    if (x < RB * NT) {
+      f32x4 y = *reinterpret_cast<const f32x4*>(part[0][x][lane]);
+#pragma unroll
+      for (int w = 1; w < kLoraWaves; ++w) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(part[w][x][lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] += z[i];
+      }
+      if (p.splits == 1) finish_tile(x, y);
+      else store16_coherent(y, mine, (uint32_t)(x * 64 + lane) * 16);
+    }
+  }
+  if (p.splits == 1) return;
+  if (!workgroup_arrive_last(p.counters + tile_no * p.chunks + chunk, (uint32_t)p.splits, &flag)) return;
+#pragma unroll
+  for (int n = 0; n < (RB * NT + 3) / 4; ++n) {
+    const int x = n * kLoraWaves + wave;
+    if (x < RB * NT) {
+      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+      for (int s0 = 0; s0 < p.splits; s0 += 8) {   // eight parts in flight
+        f32x4 z[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          z[u] = load16_coherent(make_rsrc(p.partial + (first_part + min(s0 + u, p.splits - 1)) * (kPartBytes / 4), kPartBytes),
+                                 (uint32_t)(x * 64 + lane) * 16);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] += s0 + u < p.splits ? z[u][i] : 0.f;
+      }
+      finish_tile(x, y);
+    }
   }
 }
 
-// out = base + s * B y for RB * 16 rows of one adapter and 64 columns at a time per wave.
-// Columns are the rows of the product and tokens its columns: row i of block j stands for
-// column 16 (i / 4) + 4 j + i % 4, so that a lane ends with 16 consecutive columns of one
-// token. y is brought near 1 by a power of two per token and goes in as two 16-bit terms
-// (the rounded value and the rest, good to 2^-22 or 2^-16 of it): they lie one after the
-// other along the product's inner length, against B twice, so that ranks up to 16 take no
-// more products for it. KS: steps of 32 of that length.
-template <class F, int RB, int KS>
+// out = base + s * B y: a wave takes a tile of RB * 16 rows and 64 columns at a time, the
+// four waves of a workgroup columns next to each other. Columns are the rows of the
+// product and tokens its columns: row i of block j stands for column 32 (j / 2) + 8 (i / 4)
+// + 4 (j % 2) + i % 4, so that a lane ends with eight consecutive columns of one token
+// twice, and four lanes with 64 bytes. y is brought near 1 by a power of two per token and
+// goes in as two 16-bit terms (the rounded value and the rest, good to 2^-22 or 2^-16 of
+// it), each with a product of its own. Ranks up to 16 leave half of a product's inner
+// length of 32 free: there the terms lie one after the other, against B twice (PAIRED),
+// and cost one product. KS: steps of 32 ranks.
+template <class F, int RB, int KS, bool PAIRED>
 __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int parts = p.wide ? 4 / RB : 1;   // workgroups of a tile's rows
-  const int tile_no = blockIdx.x % (uint32_t)p.cap, rest = blockIdx.x / (uint32_t)p.cap;
-  const int row_part = rest % parts, group = rest / parts;
-  LoraTile t = lora_tile(p, tile_no);
-  const int skip = row_part * RB * 16;
-  t.first += skip;
-  t.rows = min(t.rows - skip, RB * 16);
+  // workgroups that run together take the columns of the same rows
+  const uint32_t groups = p.group_begin[p.slices];
+  const int tile_no = blockIdx.x / groups, group = blockIdx.x - tile_no * groups;
+  const LoraTile t = RB == 1 ? lora_tile(p, tile_no, p.tiles16, 2) : lora_tile(p, tile_no, p.tiles64, 3);
   if (t.rows <= 0 || (t.adapter < 0 && p.in_place)) return;
   using T = typename F::T;
 
   int slice = 0;
   while (slice + 1 < p.slices && group >= p.group_begin[slice + 1]) ++slice;
   const int col_end = p.col_begin[slice + 1];
-  int col = p.col_begin[slice] + ((group - p.group_begin[slice]) * p.group_cols + wave) * kLoraCols;
-  const int group_end = min(col_end, p.col_begin[slice] + (group - p.group_begin[slice] + 1) * p.group_cols * kLoraCols);
+  const int first_col = p.col_begin[slice] + (group - p.group_begin[slice]) * p.group_cols * kLoraCols;
+  const int group_end = min(col_end, first_col + p.group_cols * kLoraCols);
+  int col = first_col + wave * kLoraCols;
+  const bool mine = col < group_end;   // this wave has columns
 
-  int64_t row[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) row[b] = p.plan[16 + t.first + min(16 * b + c, t.rows - 1)];
-
-  // ---- y as the second operand
-  const int eights = t.adapter < 0 ? 0 : t.rank / 8;   // of ranks
-  u32x4 y[RB][KS];
-  float factor[RB];
-  int chunk[KS];   // eight of ranks of this lane in each step; -1: none
-#pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    const int q = 4 * s + h;
-    chunk[s] = q < eights ? q : q < 2 * eights ? q - eights : -1;
-  }
-  const float scale = t.adapter < 0 || !p.scales ? 1.f : p.scales[t.adapter];
+  const T* base_row[RB];
+  T* out_row[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
-    f32x4 v[KS][2];
-    const int r = t.first + min(16 * b + c, t.rows - 1);
-    const int64_t row_elems = (int64_t)p.slices * p.rank_tiles * 16;
-    const float* src = p.partial + r * row_elems + slice * p.rank_tiles * 16;
-    float top = 0.f;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      v[s][0] = v[s][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (chunk[s] >= 0) {
-        for (int u = 0; u < p.splits; ++u) {
-          const f32x4* z = reinterpret_cast<const f32x4*>(src + u * p.tokens * row_elems + chunk[s] * 8);
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[s][x][i] += z[x][i];
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[s][x][i]));
-    }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // 2^e <= top < 2^(e+1) for normal values; an infinite or NaN sum stays what it is
-    const int e = min(max((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127, -100), 100);
-    const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
-    factor[b] = scale * __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const bool rest_of = 4 * s + h >= eights;
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float v0 = v[s][x][2 * i] * down, v1 = v[s][x][2 * i + 1] * down;
-          const uint32_t hi = F::pack(v0, v1);
-          y[b][s][2 * x + i] = rest_of ? F::pack(v0 - F::lo(hi), v1 - F::hi(hi)) : hi;
-        }
-    }
+    const int64_t row = p.plan[16 + t.first + min(16 * b + c, t.rows - 1)];
+    base_row[b] = static_cast<const T*>(p.base) + row * p.base_stride + 8 * h;
+    out_row[b] = static_cast<T*>(p.out) + row * p.out_stride + 8 * h;
   }
-
-  // ---- columns
-  const T* b0 = static_cast<const T*>(p.b) + max(0, t.adapter) * p.b_stride;
-  for (; col < group_end; col += kLoraWaves * kLoraCols) {
-    f32x4 acc[RB][4];
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 base[RB][2];
-    const int mine = col + 16 * h;   // this lane's columns
+  u32x4 base[RB][2];
+  auto load_base = [&](int at) {
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         base[b][x] = u32x4{0, 0, 0, 0};
-        if (p.base && mine + 8 * x < col_end)
-          base[b][x] = *reinterpret_cast<const u32x4*>(static_cast<const T*>(p.base) + row[b] * p.base_stride + mine + 8 * x);
+        if (p.base && 16 * b < t.rows && at + 32 * x + 8 * h < col_end)
+          base[b][x] = *reinterpret_cast<const u32x4*>(base_row[b] + at + 32 * x);
       }
+  };
+  if (mine) load_base(col);
+
+  // ---- B: the eight of ranks of this lane in each step
+  const int eights = t.adapter < 0 ? 0 : t.rank / 8;
+  const T* b_rows = static_cast<const T*>(p.b) + max(0, t.adapter) * p.b_stride;
+  int chunk[KS];   // -1: none
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int q = 4 * s + h;
+    chunk[s] = q < eights ? q : PAIRED && q < 2 * eights ? q - eights : -1;
+  }
+  u32x4 w[4][KS];
+  auto load_b = [&](int at) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = at + 32 * (j / 2) + 8 * (c / 4) + 4 * (j % 2) + c % 4;
+      const T* b_row = b_rows + (int64_t)min(n, col_end - 1) * p.rank;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        w[j][s] = u32x4{0, 0, 0, 0};
+        if (chunk[s] >= 0) w[j][s] = *reinterpret_cast<const u32x4*>(b_row + chunk[s] * 8);
+      }
+    }
+  };
+  if (mine) load_b(col);
+
+  // ---- y as the second operand, in LDS: both terms of each step, or (PAIRED) the two in one.
+  // Wave w prepares row blocks w, w + 4, ...
+  __shared__ __attribute__((aligned(16))) u32x4 terms[RB][KS][PAIRED ? 1 : 2][64];
+  __shared__ float factors[RB][16];
+#pragma unroll
+  for (int n = 0; n < (RB + kLoraWaves - 1) / kLoraWaves; ++n) {
+    const int b = n * kLoraWaves + wave;
+    if (b >= RB || 16 * b >= t.rows || t.adapter < 0) continue;
+    f32x4 v[KS][2];
+    const float* src = p.y + ((int64_t)(t.first + min(16 * b + c, t.rows - 1)) * p.slices + slice) * p.rank_tiles * 16;
+    float top = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        v[s][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (chunk[s] >= 0) v[s][x] = *reinterpret_cast<const f32x4*>(src + chunk[s] * 8 + 4 * x);
+      }
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[s][x][e]));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    // 2^e <= top < 2^(e+1) for normal values; an infinite or NaN sum stays what it is
+    const int e = min(max((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127, -100), 100);
+    const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+    if (h == 0) factors[b][c] = (p.scales ? p.scales[t.adapter] : 1.f) * __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      if (4 * s < 2 * eights) {
+      u32x4 hi, lo;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = min(col + 16 * (c / 4) + 4 * j + c % 4, col_end - 1);
-          u32x4 w = {0, 0, 0, 0};
-          if (chunk[s] >= 0) w = *reinterpret_cast<const u32x4*>(b0 + (int64_t)n * p.rank + chunk[s] * 8);
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int b = 0; b < RB; ++b) acc[b][j] = F::mfma16(w, y[b][s], acc[b][j]);
+        for (int i = 0; i < 2; ++i) {
+          const float v0 = v[s][x][2 * i] * down, v1 = v[s][x][2 * i + 1] * down;
+          hi[2 * x + i] = F::pack(v0, v1);
+          lo[2 * x + i] = F::pack(v0 - F::lo(hi[2 * x + i]), v1 - F::hi(hi[2 * x + i]));
+        }
+      if constexpr (PAIRED) {
+        terms[b][s][0][lane] = h >= eights ? lo : hi;
+      } else {
+        terms[b][s][0][lane] = hi;
+        terms[b][s][1][lane] = lo;
+      }
+    }
+  }
+  __syncthreads();
+  if (!mine) return;
+
+  // ---- columns
+  for (;;) {
+    const int done = col;
+    u32x4 o[RB][2];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      if (16 * b < t.rows) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          if (4 * s < eights) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[j] = F::mfma16(w[j][s], terms[b][s][0][lane], acc[j]);
+              if constexpr (!PAIRED) acc[j] = F::mfma16(w[j][s], terms[b][s][1][lane], acc[j]);
+            }
+          }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[b][x] = base[b][x];   // as it is without an adapter
+          if (t.adapter >= 0) {
+            const float factor = factors[b][c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const f32x4 v = acc[2 * x + i / 2];
+              o[b][x][i] = F::pack(F::lo(base[b][x][i]) + factor * v[2 * (i % 2)],
+                                   F::hi(base[b][x][i]) + factor * v[2 * (i % 2) + 1]);
+            }
+          }
         }
       }
+    }
+    col += kLoraWaves * kLoraCols;
+    const bool more = col < group_end;
+    if (more) {
+      load_base(col);
+      load_b(col);
     }
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        u32x4 o = base[b][x];   // as it is without an adapter
-        if (t.adapter >= 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 v = acc[b][2 * x + i / 2];
-            o[i] = F::pack(F::lo(base[b][x][i]) + factor[b] * v[2 * (i % 2)],
-                           F::hi(base[b][x][i]) + factor[b] * v[2 * (i % 2) + 1]);
-          }
-        }
-        if (16 * b + c < t.rows && mine + 8 * x < col_end)
-          *reinterpret_cast<u32x4*>(static_cast<T*>(p.out) + row[b] * p.out_stride + mine + 8 * x) = o;
-      }
+      for (int x = 0; x < 2; ++x)
+        if (16 * b + c < t.rows && done + 32 * x + 8 * h < col_end)
+          *reinterpret_cast<u32x4*>(out_row[b] + done + 32 * x) = o[b][x];
+    if (!more) break;
   }
 }
 
@@ -355,21 +439,20 @@ void shrink_tiles(const LoraArgs& a, int chunk_tiles, dim3 grid, hipStream_t s) 
   else hipLaunchKernelGGL((lora_shrink<F, RB, 4>), grid, dim3(256), 0, s, a);
 }
 
-// Tiles of 64 rows stay whole while y fits the registers beside the sums (ranks up to 64).
+template <class F, int KS, bool PAIRED>
+void expand_tiles(const LoraArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.tall_b ? a.cap64 : a.cap16) * a.group_begin[a.slices]));
+  if (a.tall_b) hipLaunchKernelGGL((lora_expand<F, 4, KS, PAIRED>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((lora_expand<F, 1, KS, PAIRED>), grid, dim3(256), 0, s, a);
+}
+
 template <class F>
-void expand_ranks(const LoraArgs& a, unsigned blocks, hipStream_t s) {
-  const int steps = (a.rank + 15) / 16;
-  if (a.wide && steps <= 1) hipLaunchKernelGGL((lora_expand<F, 4, 1>), dim3(blocks), dim3(256), 0, s, a);
-  else if (a.wide && steps <= 2) hipLaunchKernelGGL((lora_expand<F, 4, 2>), dim3(blocks), dim3(256), 0, s, a);
-  else if (a.wide && steps <= 4) hipLaunchKernelGGL((lora_expand<F, 4, 4>), dim3(blocks), dim3(256), 0, s, a);
-  else {
-    const dim3 grid(blocks * (a.wide ? 4 : 1));
-    if (steps <= 1) hipLaunchKernelGGL((lora_expand<F, 1, 1>), grid, dim3(256), 0, s, a);
-    else if (steps <= 2) hipLaunchKernelGGL((lora_expand<F, 1, 2>), grid, dim3(256), 0, s, a);
-    else if (steps <= 4) hipLaunchKernelGGL((lora_expand<F, 1, 4>), grid, dim3(256), 0, s, a);
-    else if (steps <= 8) hipLaunchKernelGGL((lora_expand<F, 1, 8>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((lora_expand<F, 1, 16>), grid, dim3(256), 0, s, a);
-  }
+void expand_ranks(const LoraArgs& a, hipStream_t s) {
+  if (a.rank <= 16) expand_tiles<F, 1, true>(a, s);
+  else if (a.rank <= 32) expand_tiles<F, 1, false>(a, s);
+  else if (a.rank <= 64) expand_tiles<F, 2, false>(a, s);
+  else if (a.rank <= 128) expand_tiles<F, 4, false>(a, s);
+  else expand_tiles<F, 8, false>(a, s);
 }
 
 }  // namespace
@@ -380,15 +463,14 @@ hipError_t launch_lora_plan(const LoraPlanArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& a, bool bf16, int chunk_tiles, hipStream_t s) {
-  const dim3 grid((unsigned)(a.cap * a.chunks * a.splits));
-  if (a.wide) bf16 ? shrink_tiles<BF16, 4>(a, chunk_tiles, grid, s) : shrink_tiles<F16, 4>(a, chunk_tiles, grid, s);
+  const dim3 grid((unsigned)((a.tall_a ? a.cap64 : a.cap16) * a.chunks * a.splits));
+  if (a.tall_a) bf16 ? shrink_tiles<BF16, 4>(a, chunk_tiles, grid, s) : shrink_tiles<F16, 4>(a, chunk_tiles, grid, s);
   else bf16 ? shrink_tiles<BF16, 1>(a, chunk_tiles, grid, s) : shrink_tiles<F16, 1>(a, chunk_tiles, grid, s);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_expand(const LoraArgs& a, bool bf16, hipStream_t s) {
-  const unsigned blocks = (unsigned)(a.cap * a.group_begin[a.slices]);
-  bf16 ? expand_ranks<BF16>(a, blocks, s) : expand_ranks<F16>(a, blocks, s);
+  bf16 ? expand_ranks<BF16>(a, s) : expand_ranks<F16>(a, s);
   return hipGetLastError();
 }
 

@@ -51,21 +51,34 @@ bool valid_stride(int64_t rows, int64_t stride, int64_t cols) {
 qg::LoraDecomposition decompose(int64_t tokens, int64_t adapters, int64_t K, int32_t rank, int32_t slices) {
   qg::LoraDecomposition d;
   const qg::LoraPlanLayout l = qg::lora_plan_layout(tokens, adapters);
-  d.wide = tokens > 256;
-  d.cap = d.wide ? l.cap64 : l.cap16;
+  // Tiles of 64 rows read the adapter's matrices once for four times the rows, tiles of 16
+  // leave more workgroups and fewer empty rows. Measured, us (16 / 64 rows; 4096 to 11008,
+  // five adapters unless stated):
+  //  - A x: 1003 rows, rank 64 10.3 / 15.6; 1500 of 8192 values, rank 32 15.4 / 13.8; 2048,
+  //    rank 64 18.6 / 16.0, rank 16 9.9 / 9.3; 4096, rank 128 55.5 / 31.4.
+  //  - its product with B, ranks above 32: 512 rows of 40 adapters 18.1 / 21.5, 1003 rows
+  //    23.3 / 21.7, 2048 40.1 / 36.9, 4096, rank 128 127 / 76; ranks to 32, whose B is
+  //    little: 1500 rows 19.3 / 21.4, 2048 20.8 / 25.6, 8192 to 8192 columns 61 / 55.
+  d.tall_a = tokens > 1024;
+  d.tall_b = tokens > (rank > 32 ? 768 : 2560);
+  const int64_t cap = d.tall_a ? l.cap64 : l.cap16;
   d.rank_tiles = (rank + qg::kLoraRankTile - 1) / qg::kLoraRankTile;
   const int64_t tiles = (int64_t)slices * d.rank_tiles;
   d.chunk_tiles = tiles >= 3 ? 4 : (int)tiles;
   d.chunks = (int)((tiles + d.chunk_tiles - 1) / d.chunk_tiles);
-  // Parts of K: about two workgroups per compute unit, as far as the parts' sums stay a
-  // quarter of x's bytes and each of a workgroup's four waves keeps 32 of K.
-  const int64_t want = 2 * qg::device_cu_count() / std::max<int64_t>(1, d.cap * d.chunks);
-  const int64_t most = std::min<int64_t>({(K + 127) / 128, std::max<int64_t>(1, K / (8 * tiles * 16)), 32});
-  const int64_t splits = std::max<int64_t>(1, std::min(want, most));
-  d.split_k = (int)(((K + splits - 1) / splits + 127) / 128 * 128);
+  // Parts of K: up to two workgroups per compute unit, which are resident at once, each of
+  // whole units of K (a run of steps for each of its four waves). 64 rows of 64 adapters, 48
+  // ranks on 8192: in 8 parts 13.6 us, in 4 13.8, in 6 uneven ones 17.1, in 16 20. More tiles
+  // than the workspace has counters fill the device without a split.
+  const int64_t unit = d.tall_a ? 256 : 512, units = (K + unit - 1) / unit;
+  int64_t want = std::max<int64_t>(1, 2 * qg::device_cu_count() / std::max<int64_t>(1, cap * d.chunks));
+  if (cap * d.chunks > qg::kMaxCounters) want = 1;
+  d.split_k = (int)((units + want - 1) / want * unit);
   d.splits = (int)((K + d.split_k - 1) / d.split_k);
-  d.partial_offset = qg::kCounterBytes;
-  d.ws_bytes = d.partial_offset + (size_t)d.splits * tokens * tiles * 16 * 4;
+  d.y_offset = qg::kCounterBytes;
+  d.partial_offset = d.y_offset + qg::align256((size_t)tokens * tiles * 16 * 4);
+  const size_t part = (size_t)(d.tall_a ? 4 : 1) * d.chunk_tiles * 1024;
+  d.ws_bytes = d.partial_offset + (d.splits > 1 ? (size_t)(cap * d.chunks * d.splits) * part : 0);
   return d;
 }
 
@@ -131,27 +144,33 @@ int run_lora(const qgemm_lora_call& g) {
   a.scales = w->scales;
   a.ranks = w->ranks;
   a.plan = static_cast<const int32_t*>(g.plan);
-  a.partial = reinterpret_cast<float*>(static_cast<char*>(g.workspace) + d.partial_offset);
+  char* ws_base = static_cast<char*>(g.workspace);
+  a.counters = reinterpret_cast<uint32_t*>(ws_base);
+  a.y = reinterpret_cast<float*>(ws_base + d.y_offset);
+  a.partial = reinterpret_cast<float*>(ws_base + d.partial_offset);
   a.tokens = (int32_t)g.num_tokens;
   a.adapters = w->num_adapters;
   a.k = (int32_t)w->K;
   a.n = (int32_t)w->N;
   a.rank = w->rank;
   a.slices = w->slices;
-  a.tiles_at = (int32_t)(d.wide ? l.tiles64 : l.tiles16);
-  a.cap = (int32_t)d.cap;
-  a.wide = d.wide;
+  a.tiles16 = (int32_t)l.tiles16;
+  a.tiles64 = (int32_t)l.tiles64;
+  a.cap16 = (int32_t)l.cap16;
+  a.cap64 = (int32_t)l.cap64;
+  a.tall_a = d.tall_a;
+  a.tall_b = d.tall_b;
   a.rank_tiles = d.rank_tiles;
   a.splits = d.splits;
   a.split_k = d.split_k;
   a.chunks = d.chunks;
   a.in_place = g.base && in_place;
-  // Columns: each wave takes up to eight tiles of 64, fewer where that would leave less
-  // than 16 waves per compute unit; more where the grid would pass 2^22 workgroups.
+  // Columns: a wave takes one tile of 64, two where that leaves 16 waves per compute unit
+  // (8192 rows, 8192 to 8192, rank 16: one 58 us, two 55, four 60; 64 rows of 64 adapters
+  // 9.4, 7.7, 8.6); more where the grid would pass 2^20 workgroups.
   const int64_t col_tiles = (w->N + qg::kLoraCols - 1) / qg::kLoraCols;
-  int64_t each = d.cap * col_tiles / (16 * qg::device_cu_count());
-  each = std::max<int64_t>(1, std::min<int64_t>(each, 8));
-  while (d.cap * (col_tiles / (qg::kLoraWaves * each) + w->slices) > (int64_t(1) << 20)) each *= 2;
+  int64_t each = std::max<int64_t>(1, std::min<int64_t>((d.tall_b ? l.cap64 : l.cap16) * col_tiles / (16 * qg::device_cu_count()), 2));
+  while (l.cap16 * (col_tiles / (qg::kLoraWaves * each) + w->slices) > (int64_t(1) << 20)) each *= 2;
   a.group_cols = (int32_t)(qg::kLoraWaves * each);
   for (int i = 0; i < w->slices; ++i) {
     const int64_t tiles = (w->widths[i] + qg::kLoraCols - 1) / qg::kLoraCols;

@@ -27,8 +27,9 @@ struct LoraPlanLayout {
 inline LoraPlanLayout lora_plan_layout(int64_t tokens, int64_t adapters) {
   LoraPlanLayout l;
   const int64_t runs = tokens < adapters + 1 ? tokens : adapters + 1;
-  l.cap16 = tokens / 16 + runs;
-  l.cap64 = tokens / 64 + runs;
+  // a run of n rows takes at most n / 16 + 1 tiles, and no more than n
+  l.cap16 = tokens < tokens / 16 + runs ? tokens : tokens / 16 + runs;
+  l.cap64 = tokens < tokens / 64 + runs ? tokens : tokens / 64 + runs;
   l.perm = 16;
   l.tiles16 = (l.perm + tokens + 3) / 4 * 4;
   l.tiles64 = l.tiles16 + 4 * l.cap16;
@@ -53,11 +54,13 @@ struct LoraArgs {
   const float* scales;
   const int32_t* ranks;
   const int32_t* plan;
-  float* partial;         // [split][sorted row][slices][rank_tiles * 16]
+  uint32_t* counters;     // one per tile and chunk, zero between calls
+  float* partial;         // [tile][chunk][split], in fragment order
+  float* y;               // [sorted row][slices][rank_tiles * 16]
   int32_t tokens, adapters, k, n, rank, slices;
-  int32_t tiles_at;       // word offset of the tiles in the plan
-  int32_t cap;            // most tiles
-  int32_t wide;           // tiles of 64 rows (0: of 16)
+  int32_t tiles16, tiles64;   // word offsets of the tiles in the plan
+  int32_t cap16, cap64;       // most tiles
+  int32_t tall_a, tall_b;     // tiles of 64 rows for the first, the second product (0: of 16)
   int32_t rank_tiles;     // of one slice
   int32_t splits, split_k;
   int32_t chunks;         // shrink: workgroups that share a tile's ranks
@@ -68,10 +71,9 @@ struct LoraArgs {
 };
 
 struct LoraDecomposition {
-  bool wide = false;
-  int64_t cap = 0;
+  bool tall_a = false, tall_b = false;   // tiles of 64 rows (of 16) for the two products
   int rank_tiles = 1, chunk_tiles = 1, chunks = 1, splits = 1, split_k = 0;
-  size_t partial_offset = 0, ws_bytes = 0;
+  size_t y_offset = 0, partial_offset = 0, ws_bytes = 0;
 };
 
 hipError_t launch_lora_plan(const LoraPlanArgs& a, hipStream_t s);

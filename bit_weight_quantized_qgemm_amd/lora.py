@@ -30,22 +30,6 @@ class _AdaptersStruct(ctypes.Structure):
 _lora_call = struct.Struct("@2PqPNPqPqqPNP").pack
 
 
-class _On:
-    """Makes a device the current one for a call, where it is not."""
-
-    def __init__(self, index: int):
-        torch = _torch()
-        self._guard = None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *error):
-        if self._guard is not None:
-            self._guard.__exit__(*error)
-
-
 class LoraAdapters:
     """The adapters of one projection, as a pool that requests choose from: a [adapters][rank][K] (or
     [adapters][slices][rank][K]) and b [adapters][N][rank], float16 or bfloat16, each adapter contiguous; scales float32
@@ -81,7 +65,8 @@ class LoraAdapters:
         self.device, self.dtype, self._index = a.device, a.dtype, a.get_device()
         self.num_adapters, self.slices, self.rank, self.K, self.N = n, slices, rank, K, N
         self.widths = tuple(widths)
-        self._empty, self._stream = torch.empty, torch._C._cuda_getCurrentRawStream
+        # what every call looks up, at hand
+        self._empty, self._stream, self._current = torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         self._struct = _AdaptersStruct(a.data_ptr(), b.data_ptr(), a.stride(0), b.stride(0),
                                        0 if scales is None else scales.data_ptr(), 0 if ranks is None else ranks.data_ptr(),
                                        K, N, (ctypes.c_int64 * MAX_SLICES)(*widths), n, rank, slices,
@@ -118,7 +103,7 @@ class LoraBatch:
         torch = _torch()
         if ids.dtype != torch.int32 or ids.shape != (self.rows,) or ids.device != self.device or not ids.is_contiguous():
             raise ValueError(f"ids must be a contiguous int32 tensor of {self.rows} rows on {self.device}")
-        with _On(self._index):
+        with torch.cuda.device(self._index):
             _check(lib().qgemm_lora_plan(ctypes.c_void_p(ids.data_ptr()), self.rows, self.num_adapters,
                                          ctypes.c_void_p(self._address), self._nbytes,
                                          ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(self._index))),
@@ -145,6 +130,19 @@ def _matrix(t, name: str, rows: int, cols: int, w: LoraAdapters):
     return t.data_ptr(), rs
 
 
+def _launch(xa, ba, oa, rows: int, adapters: LoraAdapters, batch: LoraBatch, workspace):
+    # a size depends on the device's compute units: looked up with it current
+    nbytes = adapters._ws_bytes.get(rows)
+    if nbytes is None:
+        nbytes = adapters._ws_bytes[rows] = lora_workspace_bytes(rows, adapters.num_adapters, adapters.K, adapters.N,
+                                                                 adapters.rank, adapters.slices)
+    if nbytes == 0:
+        return 0   # no rows
+    ws, wsb = (workspace or _default_ws).get(nbytes, adapters.device)
+    return lib().qgemm_lora(_lora_call(adapters._address, *xa, batch._address, batch._nbytes, *ba, *oa, rows, ws.data_ptr(),
+                                       wsb, adapters._stream(adapters._index)))
+
+
 def lora(x, adapters: LoraAdapters, batch: LoraBatch, base=None, out=None, workspace: Workspace | None = None):
     """base + scale * (x A^T) B^T with each row's own adapter: x [rows][K], base (or None) and out [rows][N] of any row
     strides. out may be base (the shared product's output, added to in place); rows without an adapter keep their base.
@@ -164,16 +162,11 @@ def lora(x, adapters: LoraAdapters, batch: LoraBatch, base=None, out=None, works
         oa = (out.data_ptr(), adapters.N)
     else:
         oa = _matrix(out, "out", rows, adapters.N, adapters)
-    with _On(adapters._index):
-        # a size depends on the device's compute units: looked up with it current
-        nbytes = adapters._ws_bytes.get(rows)
-        if nbytes is None:
-            nbytes = adapters._ws_bytes[rows] = lora_workspace_bytes(rows, adapters.num_adapters, adapters.K, adapters.N,
-                                                                     adapters.rank, adapters.slices)
-        ws, wsb = (workspace or _default_ws).get(nbytes, adapters.device)
-        call = _lora_call(adapters._address, *xa, batch._address, batch._nbytes, *ba, *oa, rows,
-                          0 if ws is None else ws.data_ptr(), wsb, adapters._stream(adapters._index))
-        status = lib().qgemm_lora(call)
+    if adapters._current() == adapters._index:
+        status = _launch(xa, ba, oa, rows, adapters, batch, workspace)
+    else:
+        with _torch().cuda.device(adapters._index):
+            status = _launch(xa, ba, oa, rows, adapters, batch, workspace)
     if status:
         _check(status, "qgemm_lora")
     return out

@@ -109,11 +109,14 @@ def test_plans_hold_the_most_tiles(T, n):
 
 
 def test_workspace_sizes():
-    for args in ((1, 8, 4096, 4096, 16, 1), (64, 66, 8192, 10240, 16, 3), (65535, 4096, 8192, 8192, 256, 8)):
+    for args in ((1, 8, 4096, 4096, 16, 1), (64, 66, 8192, 10240, 16, 3), (1003, 7, 4096, 11008, 64, 1),
+                 (8192, 5, 8192, 8192, 16, 1), (65535, 4096, 8192, 8192, 256, 8)):
         T, n, K, N, r, s = args
         got = qg.lora_workspace_bytes(*args)
-        sums = 4 * T * s * -(-r // 16) * 16
-        assert got >= 65536 + sums and (got - 65536) % sums == 0 and (got - 65536) // sums <= 32
+        y = 4 * T * s * -(-r // 16) * 16
+        assert got >= 65536 + y
+        # parts of K: whole fragments for every tile, at most 1024 workgroups' worth of 16 KB
+        assert got <= 65536 + y + 256 + 1024 * 16384
     assert qg.lora_workspace_bytes(0, 1, 64, 64, 8, 1) == 0
     for bad in ((-1, 1, 64, 64, 8, 1), (1, 0, 64, 64, 8, 1), (1, 1, 60, 64, 8, 1), (1, 1, 64, 60, 8, 1), (1, 1, 64, 64, 9, 1),
                 (1, 1, 64, 64, 8, 9)):
