@@ -23,7 +23,7 @@ PROBES_LIB = os.path.join(HERE, "libqgemm_probes.so")
 PROBES_SOURCES = ["probes.hip"]
 SOURCES = ["api.cpp", "repack.hip", "w4a16.hip", "w4a8.hip", "w2w4.hip", "wide.hip", "quant.hip", "w4g.hip", "sp24.hip",
            "bitplane_lo.hip", "bitplane_hi.hip", "noalloc.hip", "attn_api.cpp", "rope_append.hip", "attn_decode.hip",
-           "attn_prefill.hip", "attn_shared.hip", "attn_decode_own.hip", "attn_prefill_own.hip", "lora_api.cpp", "lora.hip"]
+           "attn_prefill.hip", "attn_shared_decode.hip", "attn_shared_prefill.hip", "lora_api.cpp", "lora.hip"]
 ARCH = "gfx950"
 
 

@@ -208,14 +208,20 @@ int prefill_step(int head_dim) { return head_dim <= 128 ? 4 : 2; }
 // order they end: then the mean work counts, and the longest tile (4096 new tokens,
 // 20/20 heads of 80, 640 row tiles: 95 us, in two parts 122).
 // mean: of a row tile's visible part, in the whole.
-int prefill_parts(int64_t row_tiles, int part_rows, int64_t blocks, int head_dim, bool even, double mean) {
+// cost (may be NULL): us that the parts take by this.
+int prefill_parts(int64_t row_tiles, int part_rows, int64_t blocks, int head_dim, bool even, double mean,
+                  double* cost_out = nullptr) {
   const int kStep = prefill_step(head_dim);
   const int cus = qg::device_cu_count();
   int best = 1;
-  if (row_tiles > 4 * cus) return best;
-  const int steps = (int)((blocks + kStep - 1) / kStep), tiles = (int)row_tiles;
-  const double part_mb = (double)tiles * part_rows * head_dim * 4e-6;
   const double alone = head_dim <= 64 ? 0.9 : 1.25, shared = head_dim <= 64 ? 0.65 : 1.15;
+  const int steps = (int)((blocks + kStep - 1) / kStep);
+  if (row_tiles > 4 * cus) {
+    if (cost_out) *cost_out = shared * mean * steps * (double)row_tiles / cus;
+    return best;
+  }
+  const int tiles = (int)row_tiles;
+  const double part_mb = (double)tiles * part_rows * head_dim * 4e-6;
   double least = 0;
   for (int s = 1; s <= steps && s * tiles <= 8 * cus && s <= 2 * cus; s += s < 32 ? 1 : 16) {
     const int turns = (steps + s - 1) / s, on_unit = (tiles * s + cus - 1) / cus;
@@ -227,6 +233,7 @@ int prefill_parts(int64_t row_tiles, int part_rows, int64_t blocks, int head_dim
       best = s;
     }
   }
+  if (cost_out) *cost_out = least;
   return best;
 }
 
@@ -252,53 +259,88 @@ struct Sharing {
 };
 std::atomic<int> g_force_sharing{0};   // 1: always, 2: never
 
-// Whether the shared tokens are computed apart.
-bool worth_sharing(int64_t num_seqs, int64_t num_groups, int64_t max_shared) {
-  const int force = g_force_sharing.load();
-  if (num_groups == 0 || max_shared < qg::kTokBlock || force == 2) return false;
-  return force == 1 || num_seqs >= 2 * num_groups;
-}
-
 // Sums of rows over shared tokens, next to those over own ones. Tiles of 128 rows are counted
-// as if the groups held them all and each began a tile (attn_shared.h).
+// as if the groups held them all and each began a tile (attn_shared.h). Own tokens: as many as
+// the longest context has past the longest shared run, as a guess; the kernel cuts each
+// sequence's own tokens into so many parts at most.
+//
+// The shared tokens' workgroups stand beside the own ones', which are bound by the cache's
+// stream in a decode. Measured, us, by parts of the shared tokens:
+//  - 64 sequences on 8192 + 512, 64/8 heads, bf16 (32 tiles): 4 parts 55, 7 45, 8 46, 12 55:
+//    at most one workgroup per unit, since two leave no room for others.
+//  - 96 in 4 groups on 4096 + 700, 32/8, e4m3 (32 tiles): 2 parts 54, 4 36, 5 34, 8 39, 16 48.
+//  - 128 on 2048 + 256, 32/32, fp16 (128 tiles): 1 part 68, 2 71, 4 75, 8 83: no more parts
+//    than end with the own tokens.
+// Own tokens of a decode, in waves of their own: the first case in 1, 2, 4 parts 53, 45, 46;
+// the second 50, 39, 38; the third 83, 82 in 1 and 2.
+// Where little is saved, everything is computed as in the plain call, by an estimate of both
+// (4 on 768 + 130, 32/32 heads: plain 13, shared 15; 24 prompts of up to 200 on 2048, 32/32
+// heads of 80: 121 and 116; 32 x 128 on 16384, 32/8, whose rows fill tiles by themselves: 1098
+// and 1160; 16 x 5 on 6000, 64/8: 50 and 35).
 qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, int64_t max_len, int q_heads,
                            int kv_heads, int head_dim, const Mask& mask, int64_t num_groups, int64_t max_shared,
                            bool prefill) {
   qg::SharedPlan pl;
   max_shared = std::min(max_shared, max_len) / qg::kTokBlock * qg::kTokBlock;
-  const int64_t rows = num_tokens * (q_heads / kv_heads);
-  pl.tiles = (rows / qg::kPrefillRows + num_groups) * kv_heads;
-  const int64_t row_tiles = (max_q * (q_heads / kv_heads) + qg::kPrefillRows - 1) / qg::kPrefillRows;
-  // (the join's grid has up to 32 workgroups per row tile)
-  pl.share = worth_sharing(num_seqs, num_groups, max_shared) && pl.tiles <= (INT32_MAX >> 10) &&
-             num_seqs * kv_heads * row_tiles <= INT32_MAX / 32;
+  const int mode = g_force_sharing.load(), force = g_force_splits.load();
+  const int64_t cus = qg::device_cu_count(), group = q_heads / kv_heads;
+  if (num_groups > 0 && max_shared > 0 && mode != 2 && (mode == 1 || num_seqs >= 2 * num_groups)) {
+    const int64_t own_len = std::max({max_len - max_shared, max_q, int64_t(1)});
+    const Mask own_mask = bounded_mask(own_len, mask.window, mask.sinks);
+    pl.own = prefill ? prefill_plan(num_seqs, max_q, own_len, q_heads, kv_heads, head_dim, own_mask)
+                     : decode_plan(num_seqs, own_len, q_heads, kv_heads, head_dim, own_mask);
+    const int64_t rows = num_tokens * group, blocks = max_shared / qg::kTokBlock;
+    pl.tiles = (rows / qg::kPrefillRows + num_groups) * kv_heads;
+    const int64_t live = std::max(num_groups, (rows + qg::kPrefillRows - 1) / qg::kPrefillRows) * kv_heads;
+    const int step = prefill_step(head_dim);
+    double cost;
+    int64_t parts =
+        prefill_parts(live, (int)std::min<int64_t>(rows, qg::kPrefillRows), blocks, head_dim, true, 1, &cost);
+    const int64_t turns = (blocks + step - 1) / step;
+    const double turn = head_dim <= 64 ? 0.9 : 1.25, value_mb = 4e-6 * kv_heads * head_dim;   // K and V of a token
+    if (2 * live <= cus) parts = std::min(cus / live, turns);
+    double own_cost, plain_cost;
+    if (prefill) {
+      const int64_t plain_blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), mask);
+      prefill_parts(pl.own.tiles, pl.own.part_rows, plain_blocks, head_dim, true, 1, &plain_cost);
+      const int64_t own_turns = (own_len + 16 * step - 1) / (16 * step);
+      own_cost = (head_dim <= 64 ? 0.65 : 1.15) * own_turns * (double)pl.own.tiles / cus;
+      cost = 2 * live <= cus ? turn * ((turns + parts - 1) / parts) : cost;
+      cost += own_cost;
+    } else {
+      // a wave for each part: eight waves per compute unit, each with 128 tokens at least
+      const int64_t waves = 8 * cus, most = (visible_blocks(own_len, 1, own_mask) + 7) / 8;
+      pl.own.splits = (int)std::max<int64_t>(1, std::min((waves + pl.own.tiles - 1) / std::max<int64_t>(1, pl.own.tiles), most));
+      own_cost = value_mb * num_seqs * (mask.window ? std::min(own_len, mask.window + mask.sinks) : own_len) / 5.0;
+      plain_cost = value_mb * num_seqs * (mask.window ? std::min(max_len, mask.window + mask.sinks) : max_len) / 6.0;
+      // fewest parts that end with the own tokens, of which half are taken to be there
+      int64_t least = 1;
+      while (least < parts && 9 + turn * ((turns + least - 1) / least) > 0.5 * own_cost) ++least;
+      parts = least;
+      cost = std::max(own_cost, 2 * live <= cus ? turn * ((turns + parts - 1) / parts) : cost);
+    }
+    // start and end of the shared workgroups, the join's launch, and the parts that it reads
+    cost += 9 + 3 + 1e-6 * rows * q_heads / group * head_dim * 4 * (parts + pl.own.splits) / 4.0;
+    pl.share = mode == 1 || cost < plain_cost + 4;
+    if (force) parts = pl.own.splits = force;
+    const int64_t per = (blocks + parts - 1) / parts;
+    pl.split_blocks = (int)((per + step - 1) / step * step);
+    pl.splits = (int)((blocks + pl.split_blocks - 1) / pl.split_blocks);
+    // 32-bit numbers of workgroups and waves, in all launches
+    const int64_t join = pl.own.tiles * 32 + num_seqs * (((int64_t)q_heads * head_dim + 1023) / 1024);
+    if (pl.tiles * pl.splits + pl.own.tiles * pl.own.splits + join > INT32_MAX) pl.share = false;
+  }
   if (!pl.share) {
     pl.own = prefill ? prefill_plan(num_seqs, max_q, max_len, q_heads, kv_heads, head_dim, mask)
                      : decode_plan(num_seqs, max_len, q_heads, kv_heads, head_dim, mask);
     pl.ws_bytes = pl.own.ws_bytes;
     return pl;
   }
-  // Own tokens: as many as the longest context has past the longest shared run, as a guess;
-  // the kernel cuts each sequence's own tokens into that many parts at most.
-  const int64_t own_len = std::max({max_len - max_shared, max_q, int64_t(1)});
-  const Mask own_mask = bounded_mask(own_len, mask.window, mask.sinks);
-  pl.own = prefill ? prefill_plan(num_seqs, max_q, own_len, q_heads, kv_heads, head_dim, own_mask)
-                   : decode_plan(num_seqs, own_len, q_heads, kv_heads, head_dim, own_mask);
-  const int64_t blocks = max_shared / qg::kTokBlock;
-  const int64_t live = std::max(num_groups, (rows + qg::kPrefillRows - 1) / qg::kPrefillRows) * kv_heads;
-  const int force = g_force_splits.load(), step = prefill_step(head_dim);
-  const int64_t parts =
-      force ? force : prefill_parts(live, (int)std::min<int64_t>(rows, qg::kPrefillRows), blocks, head_dim, true, 1);
-  const int64_t per = (blocks + parts - 1) / parts;
-  pl.split_blocks = (int)((per + step - 1) / step * step);
-  pl.splits = (int)((blocks + pl.split_blocks - 1) / pl.split_blocks);
   size_t end = qg::kCounterBytes;
-  if (pl.own.splits > 1 || prefill) {
-    const size_t own_parts = (size_t)pl.own.tiles * pl.own.splits;
-    pl.own.stats_offset = end;
-    pl.own.partial_offset = end + qg::align256(own_parts * pl.own.part_rows * 8);
-    end = pl.own.partial_offset + qg::align256(own_parts * pl.own.part_rows * head_dim * 4);
-  }
+  const size_t own_rows = (size_t)pl.own.tiles * pl.own.splits * pl.own.part_rows;
+  pl.own.stats_offset = end;
+  pl.own.partial_offset = end + qg::align256(own_rows * 8);
+  end = pl.own.partial_offset + qg::align256(own_rows * head_dim * 4);
   const size_t shared_rows = (size_t)pl.tiles * pl.splits * qg::kPrefillRows;
   pl.stats_offset = end;
   pl.partial_offset = end + shared_rows * 8;
@@ -437,12 +479,11 @@ int run_attn(const qgemm_attn_call& g, bool prefill, const Sharing* sharing) {
     a.shared_tiles = (int32_t)sp.tiles;
     a.shared_splits = sp.splits;
     a.shared_split_blocks = sp.split_blocks;
-    a.split_step = prefill ? prefill_step(c->head_dim) : kDecodeStep;
+    a.split_step = prefill ? prefill_step(c->head_dim) : 2;   // decode: a pair of blocks
     a.inv_shared_tiles = 1.0 / (double)sp.tiles;
-    e = qg::launch_attn_shared(a, bf16, fp8, s);
-    if (e == hipSuccess)
-      e = prefill ? qg::launch_attn_prefill_own(a, bf16, fp8, pl.tiles, s)
-                  : qg::launch_attn_decode_own(a, bf16, fp8, pl.tiles, s);
+    a.shared_blocks = (int32_t)(sp.tiles * sp.splits);
+    e = prefill ? qg::launch_attn_prefill_shared(a, bf16, fp8, pl.tiles, s)
+                : qg::launch_attn_decode_shared(a, bf16, fp8, pl.tiles, s);
   } else {
     e = prefill ? qg::launch_attn_prefill(a, bf16, fp8, pl.tiles, s)
                 : qg::launch_attn_decode(a, bf16, fp8, pl.tiles, s);

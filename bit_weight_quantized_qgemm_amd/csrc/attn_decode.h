@@ -57,18 +57,24 @@ struct PairAt {
   int rows[2];         // tokens that may be read
 };
 
-// EXACT: head_dim is DP, so that the loads' offsets need no bounds of their own. SHARED: the
-// sequence's tokens past those that it shares with others, whose sums an earlier launch left
-// in the workspace, are computed, and both are joined.
-template <class F, class PF, bool FP8, int DP, bool EXACT, bool SHARED>
-__device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, SharedArgs, AttnArgs>& p) {
+template <int DP>
+struct DecodeLds {
+  static constexpr int kOutStride = DP + 4;
+  float part[kDecodeWaves][kDecodeRows][kOutStride];
+  float part_max[kDecodeWaves][kDecodeRows], part_sum[kDecodeWaves][kDecodeRows];
+  int flag;
+};
+
+// EXACT: head_dim is DP, so that the loads' offsets need no bounds of their own. OWN: the
+// sequence's tokens past those that it shares with others, a wave for each part; the sums stay
+// in the workspace, for the join with the shared ones'. block: workgroup (OWN: wave) among
+// those of this kind.
+template <class F, class PF, bool FP8, int DP, bool EXACT, bool OWN>
+__device__ __forceinline__ void decode_body(const std::conditional_t<OWN, SharedArgs, AttnArgs>& p, int block,
+                                            DecodeLds<DP>* lds) {
   using S = DecodeShape<F, FP8, DP>;
   using T = typename F::T;
-  constexpr int kOutStride = DP + 4;
-  __shared__ float part[kDecodeWaves][kDecodeRows][kOutStride];
-  __shared__ float part_max[kDecodeWaves][kDecodeRows], part_sum[kDecodeWaves][kDecodeRows];
-  __shared__ int flag;
-
+  constexpr int kTurn = OWN ? 1 : kDecodeWaves;   // waves that take pairs in turn
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // all first parts, then all second ones: the parts that a shorter sequence does
@@ -76,7 +82,7 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
   // part number in equal shares
   const int heads = p.kv_heads * p.row_tiles;
   const int tiles = p.num_seqs * heads;
-  const int block = blockIdx.x + p.first_block;
+  if (OWN && block >= tiles * p.splits) return;
   const int split = p.splits == 1 ? 0 : divide_uniform(block, p.inv_tiles), tile = block - split * tiles;
   const int seq = divide_uniform(tile, p.inv_heads);
   const int row_tile = p.row_tiles == 1 ? 0 : (tile - seq * heads) % p.row_tiles;
@@ -88,10 +94,8 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
   const Visible see(len, p.window ? len - p.window : 0, p.window ? p.sinks : 0);
   // never more than the workspace holds (the plan covers see.blocks with p.splits)
   int parts, split_blocks, v_first = 0;
-  SharedGroup group{};
-  if constexpr (SHARED) {
-    group = group_of(p, seq);
-    const OwnBlocks own = own_blocks(see, group.shared, p.splits, p.split_step);
+  if constexpr (OWN) {
+    const OwnBlocks own = own_blocks(see, group_of(p, seq).shared, p.splits, p.split_step);
     parts = own.parts;
     split_blocks = own.split_blocks;
     v_first = own.first;
@@ -196,12 +200,12 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
     for (int i = 0; i < S::kVDims; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int pair_end = (v_end - v_first + 1) / 2;
-  int pair = split * split_blocks / 2 + wave;
+  int pair = split * split_blocks / 2 + (OWN ? 0 : wave);
   PairAt now = locate(pair);
   load_k(now);
   load_v(now);
-  PairAt next = locate(pair + kDecodeWaves);
-  for (; pair < pair_end; pair += kDecodeWaves) {
+  PairAt next = locate(pair + kTurn);
+  for (; pair < pair_end; pair += kTurn) {
     // ---- scores of the pair: lane (c, h) gets head c, tokens 4h..4h+3 of each block
     f32x4 sc[2];
 #pragma unroll
@@ -327,12 +331,31 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
     load_v(next);
     __builtin_amdgcn_sched_barrier(0);
     now = next;
-    next = locate(pair + 2 * kDecodeWaves);
+    next = locate(pair + 2 * kTurn);
   }
 
-  // ---- join the waves
   sum += __shfl_xor(sum, 16, 64);
   sum += __shfl_xor(sum, 32, 64);
+  const int64_t part_id = (int64_t)tile * p.splits + split;
+  if constexpr (OWN) {
+    if (c >= rows) return;
+    float* dst = p.partial + (part_id * p.part_rows + c) * p.head_dim;
+#pragma unroll
+    for (int j = 0; j < S::kVCols; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < S::kVDims; i += 4) {
+          const int d = j * 16 * S::kVDims + (4 * h + r) * S::kVDims + i;
+          if (EXACT || d < p.head_dim)
+            *reinterpret_cast<f32x4*>(dst + d) = f32x4{acc[j][i][r], acc[j][i + 1][r], acc[j][i + 2][r], acc[j][i + 3][r]};
+        }
+    if (h == 0) *reinterpret_cast<f32x2*>(p.stats + (part_id * p.part_rows + c) * 2) = f32x2{mref, sum};
+    return;
+  } else {
+  // ---- join the waves
+  auto& part = lds->part;
+  auto &part_max = lds->part_max, &part_sum = lds->part_sum;
   if (lane < kDecodeRows) {
     part_max[wave][lane] = mref;
     part_sum[wave][lane] = sum;
@@ -350,7 +373,6 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
   __syncthreads();
 
   const int quads = p.head_dim / 4;   // fp32 quadruples of a row
-  const int64_t part_id = (int64_t)tile * p.splits + split;
   float* stats = p.stats + part_id * p.part_rows * 2;
   const rsrc_t out_r = make_rsrc(p.partial + part_id * p.part_rows * p.head_dim, (uint32_t)(p.part_rows * p.head_dim * 4));
   for (int x = threadIdx.x; x < rows * quads; x += 256) {
@@ -370,12 +392,6 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
       for (int i = 0; i < 4; ++i) o[i] += f * y[i];
     }
     if (parts == 1) {
-      if constexpr (SHARED) {
-        RowSums r{m, total, o};
-        add_shared_parts(r, p, group, kv_head, seq - group.seq, row_tile * kDecodeRows + row, d);
-        total = r.total;
-        o = r.o;
-      }
       T* dst = static_cast<T*>(p.out) + seq * p.o_ts + (head0 + row) * p.o_hs + d;
       *reinterpret_cast<u32x2*>(dst) = finish<F>(o, total, p.v_scale);
     } else {
@@ -387,29 +403,10 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
     }
   }
   if (parts == 1) return;
-  if (!workgroup_arrive_last(p.counters + tile, (uint32_t)parts, &flag)) return;
+  if (!workgroup_arrive_last(p.counters + tile, (uint32_t)parts, &lds->flag)) return;
 
   // ---- join the parts, in part order
-  if constexpr (SHARED) {
-    const uint32_t part_bytes = (uint32_t)(p.part_rows * p.head_dim) * 4;
-    const float* tile_partial = p.partial + (int64_t)tile * p.splits * p.part_rows * p.head_dim;
-    const float* tile_stats = p.stats + (int64_t)tile * p.splits * p.part_rows * 2;
-    for (int x = threadIdx.x; x < rows * quads; x += 256) {
-      const int row = x / quads, d = 4 * (x - row * quads);
-      RowSums r;
-      add_parts(r, parts, [&](int s, f32x4& y, float& m, float& l) {
-        y = load16_coherent(make_rsrc(tile_partial + (int64_t)s * p.part_rows * p.head_dim, part_bytes),
-                            (uint32_t)(row * p.head_dim + d) * 4);
-        const float* at = tile_stats + ((int64_t)s * p.part_rows + row) * 2;
-        m = load_shared(at);
-        l = load_shared(at + 1);
-      });
-      add_shared_parts(r, p, group, kv_head, seq - group.seq, row_tile * kDecodeRows + row, d);
-      T* dst = static_cast<T*>(p.out) + seq * p.o_ts + (head0 + row) * p.o_hs + d;
-      *reinterpret_cast<u32x2*>(dst) = finish<F>(r.o, r.total, p.v_scale);
-    }
-  } else {
-    join_parts<F>(p, tile, parts, rows, [&](int r) { return seq * p.o_ts + (head0 + r) * p.o_hs; });
+  join_parts<F>(p, tile, parts, rows, [&](int r) { return seq * p.o_ts + (head0 + r) * p.o_hs; });
   }
 }
 
@@ -417,11 +414,8 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<SHARED, Sha
 // in flight take, without spills.
 template <class F, class PF, bool FP8, int DP, bool EXACT>
 __global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_decode(AttnArgs p) {
-  decode_body<F, PF, FP8, DP, EXACT, false>(p);
-}
-template <class F, class PF, bool FP8, int DP, bool EXACT>
-__global__ void __launch_bounds__(256, DP == 64 ? 4 : DP == 128 ? 3 : 1) attn_decode_own(SharedArgs p) {
-  decode_body<F, PF, FP8, DP, EXACT, true>(p);
+  __shared__ DecodeLds<DP> lds;
+  decode_body<F, PF, FP8, DP, EXACT, false>(p, blockIdx.x + p.first_block, &lds);
 }
 
 }  // namespace

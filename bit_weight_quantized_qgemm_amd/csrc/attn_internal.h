@@ -80,7 +80,8 @@ struct SharedArgs : AttnArgs {
   int32_t num_groups, max_shared;
   int32_t shared_tiles;     // tiles of 128 rows of a group and key-value head
   int32_t shared_splits;
-  int32_t shared_split_blocks;
+  int32_t shared_split_blocks;   // token blocks of a part
+  int32_t shared_blocks;    // workgroups of the shared tokens: the first ones of the launch
   int32_t split_step;       // token blocks of an own part: a multiple of this
   double inv_shared_tiles;
 };
@@ -128,9 +129,8 @@ struct SharedPlan {
 hipError_t launch_append(const AppendArgs& a, bool bf16, bool fp8, bool interleaved, hipStream_t s);
 hipError_t launch_attn_decode(const AttnArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
 hipError_t launch_attn_prefill(const AttnArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
-// The shared tokens of all groups; then each sequence's own ones, joined with them.
-hipError_t launch_attn_shared(const SharedArgs& a, bool bf16, bool fp8, hipStream_t s);
-hipError_t launch_attn_decode_own(const SharedArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
-hipError_t launch_attn_prefill_own(const SharedArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
+// The same for a batch with shared tokens (tiles: of the own ones).
+hipError_t launch_attn_decode_shared(const SharedArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
+hipError_t launch_attn_prefill_shared(const SharedArgs& a, bool bf16, bool fp8, int64_t tiles, hipStream_t s);
 
 }  // namespace qg

@@ -188,9 +188,10 @@ __device__ __forceinline__ RowTile shared_tile_of(const SharedArgs& p, int tile)
 template <PrefillMode MODE>
 using PrefillArgs = std::conditional_t<MODE == kAlone, AttnArgs, SharedArgs>;
 
-// DP: values of a head's place in LDS; DU: those that take part in the products.
+// DP: values of a head's place in LDS; DU: those that take part in the products. block:
+// workgroup among those of this kind.
 template <class F, class PF, bool FP8, int DP, int DU, bool EXACT, PrefillMode MODE>
-__device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, char* lds) {
+__device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int block, char* lds) {
   using L = PrefillLds<DP>;
   using T = typename F::T;
   constexpr int kElt = FP8 ? 1 : 2;
@@ -205,7 +206,6 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, char* l
 
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int block = blockIdx.x + p.first_block;
   int split, tile;
   if constexpr (MODE == kShared) {
     split = divide_uniform(block, p.inv_shared_tiles), tile = block - split * p.shared_tiles;
@@ -663,12 +663,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, char* l
 template <class F, class PF, bool FP8, int DP, int DU, bool EXACT>
 __global__ void __launch_bounds__(256, DP <= 128 ? 2 : 1) attn_prefill(AttnArgs p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  prefill_body<F, PF, FP8, DP, DU, EXACT, kAlone>(p, lds);
-}
-template <class F, class PF, bool FP8, int DP, int DU, bool EXACT, PrefillMode MODE>
-__global__ void __launch_bounds__(256, DP <= 128 ? 2 : 1) attn_prefill_part(SharedArgs p) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  prefill_body<F, PF, FP8, DP, DU, EXACT, MODE>(p, lds);
+  prefill_body<F, PF, FP8, DP, DU, EXACT, kAlone>(p, blockIdx.x + p.first_block, lds);
 }
 
 }  // namespace

@@ -28,10 +28,10 @@ __device__ __forceinline__ int count_up_to(int n, int x, const Entry& entry) {
 }
 
 __device__ __forceinline__ int bounded_seq(const SharedArgs& p, int seq) { return min(max(seq, 0), p.num_seqs); }
-// Tokens that a group's kernel takes as shared: whole blocks, so that both parts of a
+// Tokens taken as shared of a group that says `len`: whole blocks, so that both parts of a
 // context consist of whole ones (the rest is read through each sequence's own entries).
-__device__ __forceinline__ int shared_of(const SharedArgs& p, int group) {
-  return min(max(scalar_load(p.shared_lens + group), 0), p.max_shared) / kTokBlock * kTokBlock;
+__device__ __forceinline__ int whole_blocks(const SharedArgs& p, int len) {
+  return min(max(len, 0), p.max_shared) / kTokBlock * kTokBlock;
 }
 // First row of q of sequence seq (tokens are sequences in a call with one token each).
 __device__ __forceinline__ int token_of(const SharedArgs& p, int seq) {
@@ -42,12 +42,26 @@ struct SharedGroup {
   int group, seq;   // its number and first sequence
   int shared;       // tokens shared (0: no group)
 };
+// (up to 64 groups, all that is asked for comes in one go)
 __device__ __forceinline__ SharedGroup group_of(const SharedArgs& p, int seq) {
-  const int n = count_up_to(p.num_groups + 1, seq, [&](int i) { return p.group_start[i]; });
-  if (n < 1 || n > p.num_groups) return SharedGroup{0, 0, 0};
-  const int first = bounded_seq(p, scalar_load(p.group_start + n - 1));
+  const int lane = threadIdx.x & 63;
+  int n, first, shared;
+  if (p.num_groups <= 64) {
+    const int at = min(lane, p.num_groups - 1), start = p.group_start[at], len = p.shared_lens[at];
+    const int end = p.group_start[p.num_groups];
+    n = __popcll(__ballot(lane < p.num_groups && start <= seq));
+    if (n < 1 || (n == p.num_groups && __builtin_amdgcn_readfirstlane(end) <= seq)) return SharedGroup{0, 0, 0};
+    first = __builtin_amdgcn_readlane(start, n - 1);
+    shared = __builtin_amdgcn_readlane(len, n - 1);
+  } else {
+    n = count_up_to(p.num_groups + 1, seq, [&](int i) { return p.group_start[i]; });
+    if (n < 1 || n > p.num_groups) return SharedGroup{0, 0, 0};
+    first = scalar_load(p.group_start + n - 1);
+    shared = scalar_load(p.shared_lens + n - 1);
+  }
+  first = bounded_seq(p, first);
   if (first > seq) return SharedGroup{0, 0, 0};   // entries that fall
-  return SharedGroup{n - 1, first, shared_of(p, n - 1)};
+  return SharedGroup{n - 1, first, whole_blocks(p, shared)};
 }
 
 // Tiles of 128 rows are numbered without a count of anybody's rows: group g, whose first row
@@ -60,16 +74,30 @@ struct GroupRows {
   int shared;
 };
 __device__ __forceinline__ GroupRows group_of_tile(const SharedArgs& p, int t) {
-  auto first_tile = [&](int g) { return token_of(p, bounded_seq(p, p.group_start[g])) * p.group / kPrefillRows + g; };
-  const int n = count_up_to(p.num_groups, t, first_tile);
-  if (n < 1) return GroupRows{0, 0, 0, 0, 0};
+  const int lane = threadIdx.x & 63;
   GroupRows r;
-  r.seq = __builtin_amdgcn_readfirstlane(bounded_seq(p, p.group_start[n - 1]));
-  r.token = __builtin_amdgcn_readfirstlane(token_of(p, r.seq));
-  r.token_end = __builtin_amdgcn_readfirstlane(token_of(p, bounded_seq(p, p.group_start[n])));
+  int n;
+  if (p.num_groups <= 64) {
+    const int at = min(lane, p.num_groups - 1);
+    const int seq = bounded_seq(p, p.group_start[at]), end = bounded_seq(p, p.group_start[at + 1]), len = p.shared_lens[at];
+    const int token = token_of(p, seq), token_end = token_of(p, end);
+    n = __popcll(__ballot(lane < p.num_groups && token * p.group / kPrefillRows + lane <= t));
+    if (n < 1) return GroupRows{0, 0, 0, 0, 0};
+    r.seq = __builtin_amdgcn_readlane(seq, n - 1);
+    r.token = __builtin_amdgcn_readlane(token, n - 1);
+    r.token_end = __builtin_amdgcn_readlane(token_end, n - 1);
+    r.shared = whole_blocks(p, __builtin_amdgcn_readlane(len, n - 1));
+  } else {
+    auto first_tile = [&](int g) { return token_of(p, bounded_seq(p, p.group_start[g])) * p.group / kPrefillRows + g; };
+    n = count_up_to(p.num_groups, t, first_tile);
+    if (n < 1) return GroupRows{0, 0, 0, 0, 0};
+    r.seq = __builtin_amdgcn_readfirstlane(bounded_seq(p, p.group_start[n - 1]));
+    r.token = __builtin_amdgcn_readfirstlane(token_of(p, r.seq));
+    r.token_end = __builtin_amdgcn_readfirstlane(token_of(p, bounded_seq(p, p.group_start[n])));
+    r.shared = whole_blocks(p, scalar_load(p.shared_lens + n - 1));
+  }
   r.first_tile = r.token * p.group / kPrefillRows + n - 1;
   if (r.seq >= p.num_seqs || r.first_tile > t) r.token_end = r.token;   // entries that fall
-  r.shared = shared_of(p, n - 1);
   return r;
 }
 
@@ -120,35 +148,39 @@ struct RowSums {
   float m = kNegInf, total = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
 };
-// Adds `parts` parts to them, in order; load(s, y, m, l) gives the four sums, the maximum and
+// Adds parts s..s+N-1 to them, in order; load(s, y, m, l) gives the four sums, the maximum and
 // the sum of weights of part s.
+template <int N, class Load>
+__device__ __forceinline__ void add_batch(RowSums& r, int s, const Load& load) {
+  f32x4 y[N];
+  float ym[N], yl[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) load(s + u, y[u], ym[u], yl[u]);
+  float top = r.m;
+#pragma unroll
+  for (int u = 0; u < N; ++u) top = fmaxf(top, ym[u]);
+  const float base = top == kNegInf ? 0.f : top;
+  const float f0 = exp2_of(r.m - base);
+  r.total *= f0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.o[i] *= f0;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const float f = exp2_of(ym[u] - base);
+    r.total += f * yl[u];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.o[i] += f * y[u][i];
+  }
+  r.m = top;
+}
+// All of `parts` parts, eight in flight together.
 template <class Load>
 __device__ __forceinline__ void add_parts(RowSums& r, int parts, const Load& load) {
-  constexpr int kBatch = 8;   // parts whose loads are in flight together
-  for (int s0 = 0; s0 < parts; s0 += kBatch) {
-    f32x4 y[kBatch];
-    float ym[kBatch], yl[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) load(min(s0 + u, parts - 1), y[u], ym[u], yl[u]);
-    float top = r.m;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ym[u]);   // re-read last parts change nothing
-    const float base = top == kNegInf ? 0.f : top;
-    const float f0 = exp2_of(r.m - base);
-    r.total *= f0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.o[i] *= f0;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (s0 + u < parts) {
-        const float f = exp2_of(ym[u] - base);
-        r.total += f * yl[u];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.o[i] += f * y[u][i];
-      }
-    }
-    r.m = top;
-  }
+  int s = 0;
+  for (; parts - s >= 8; s += 8) add_batch<8>(r, s, load);
+  if (parts - s >= 4) add_batch<4>(r, s, load), s += 4;
+  if (parts - s >= 2) add_batch<2>(r, s, load), s += 2;
+  if (parts - s >= 1) add_batch<1>(r, s, load);
 }
 // Adds the shared part of a row: head `head` of the key-value head's group, of token `token`
 // of the sequences' group; values d..d+3.
