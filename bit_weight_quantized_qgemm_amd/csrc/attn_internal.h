@@ -78,12 +78,12 @@ struct SharedArgs : AttnArgs {
   float* shared_partial;    // [shared tile][shared split][kPrefillRows][head_dim]
   float* shared_stats;      // [shared tile][shared split][kPrefillRows] (maximum, sum)
   int32_t num_groups, max_shared;
-  int32_t shared_tiles;     // tiles of 128 rows of a group and key-value head
+  int32_t shared_row_tiles; // tiles of 128 rows of a group, for each key-value head
   int32_t shared_splits;
   int32_t shared_split_blocks;   // token blocks of a part
   int32_t shared_blocks;    // workgroups of the shared tokens: the first ones of the launch
   int32_t split_step;       // token blocks of an own part: a multiple of this
-  double inv_shared_tiles;
+  double inv_shared_splits;
 };
 
 struct AttnPlan {

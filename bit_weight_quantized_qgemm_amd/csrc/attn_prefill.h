@@ -172,8 +172,7 @@ __device__ __forceinline__ RowTile own_tile_of(const SharedArgs& p, int tile) {
 // A row tile of a group: its rows are those of all its sequences' new tokens, which
 // stand one after the other in q. Where positions differ, see and pos_* are for the
 // caller to fill in.
-__device__ __forceinline__ RowTile shared_tile_of(const SharedArgs& p, int tile) {
-  const int t = divide_uniform(tile, p.inv_kv_heads), kv_head = tile - t * p.kv_heads;
+__device__ __forceinline__ RowTile shared_tile_of(const SharedArgs& p, int t, int kv_head) {
   const GroupRows g = group_of_tile(p, t);
   const int all_rows = (g.token_end - g.token) * p.group;
   const int row0 = max(0, t - g.first_tile) * kPrefillRows;
@@ -208,7 +207,9 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int split, tile;
   if constexpr (MODE == kShared) {
-    split = divide_uniform(block, p.inv_shared_tiles), tile = block - split * p.shared_tiles;
+    // key-value heads innermost, and rows outermost: tiles without rows come last
+    const int x = divide_uniform(block, p.inv_kv_heads), t = divide_uniform(x, p.inv_shared_splits);
+    split = x - t * p.shared_splits, tile = t * p.kv_heads + block - x * p.kv_heads;
   } else {
     const int tiles = p.num_seqs * p.kv_heads * p.row_tiles;
     split = p.splits == 1 ? 0 : divide_uniform(block, p.inv_tiles), tile = block - split * tiles;
@@ -216,7 +217,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
   RowTile rt = [&]() {
     if constexpr (MODE == kAlone) return row_tile_of(p, tile);
     else if constexpr (MODE == kOwn) return own_tile_of(p, tile);
-    else return shared_tile_of(p, tile);
+    else return shared_tile_of(p, tile / p.kv_heads, tile % p.kv_heads);
   }();
   if (rt.rows <= 0 || split >= rt.parts) return;
 

@@ -38,35 +38,58 @@ __device__ __forceinline__ int token_of(const SharedArgs& p, int seq) {
   return p.q_start ? min(max(p.q_start[seq], 0), p.num_tokens) : seq;
 }
 
+// Tiles of 128 rows. Up to 64 groups, one per lane, they are numbered group after group by a
+// prefix sum, so that those without rows come last. Beyond, group g, whose first row is number
+// r of all, begins with tile r / 128 + g: it needs at most n / 128 + 1 tiles (rounded down) for
+// n rows, so the next one's first is past its last.
+__device__ __forceinline__ int tiles_before(const SharedArgs& p, int token, int token_end) {
+  const int lane = threadIdx.x & 63;
+  const int mine = (max(0, token_end - token) * p.group + kPrefillRows - 1) / kPrefillRows;
+  int to = lane < p.num_groups ? mine : 0;
+  const int own = to;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int x = __shfl_up(to, d, 64);
+    if (lane >= d) to += x;
+  }
+  return to - own;
+}
+
 struct SharedGroup {
   int group, seq;   // its number and first sequence
+  int token;        // its first row of q
+  int first_tile;
   int shared;       // tokens shared (0: no group)
 };
 // (up to 64 groups, all that is asked for comes in one go)
 __device__ __forceinline__ SharedGroup group_of(const SharedArgs& p, int seq) {
   const int lane = threadIdx.x & 63;
-  int n, first, shared;
+  SharedGroup g{0, 0, 0, 0, 0};
+  int n, shared;
   if (p.num_groups <= 64) {
-    const int at = min(lane, p.num_groups - 1), start = p.group_start[at], len = p.shared_lens[at];
-    const int end = p.group_start[p.num_groups];
-    n = __popcll(__ballot(lane < p.num_groups && start <= seq));
-    if (n < 1 || (n == p.num_groups && __builtin_amdgcn_readfirstlane(end) <= seq)) return SharedGroup{0, 0, 0};
-    first = __builtin_amdgcn_readlane(start, n - 1);
+    const int at = min(lane, p.num_groups - 1), raw = p.group_start[at], len = p.shared_lens[at];
+    const int raw_end = p.group_start[at + 1];
+    n = __popcll(__ballot(lane < p.num_groups && raw <= seq));
+    if (n < 1 || __builtin_amdgcn_readlane(raw_end, n - 1) <= seq) return g;
+    const int token = token_of(p, bounded_seq(p, raw)), token_end = token_of(p, bounded_seq(p, raw_end));
+    g.first_tile = __builtin_amdgcn_readlane(tiles_before(p, token, token_end), n - 1);
+    g.token = __builtin_amdgcn_readlane(token, n - 1);
+    g.seq = bounded_seq(p, __builtin_amdgcn_readlane(raw, n - 1));
     shared = __builtin_amdgcn_readlane(len, n - 1);
   } else {
     n = count_up_to(p.num_groups + 1, seq, [&](int i) { return p.group_start[i]; });
-    if (n < 1 || n > p.num_groups) return SharedGroup{0, 0, 0};
-    first = scalar_load(p.group_start + n - 1);
+    if (n < 1 || n > p.num_groups) return g;
+    g.seq = bounded_seq(p, scalar_load(p.group_start + n - 1));
+    g.token = __builtin_amdgcn_readfirstlane(token_of(p, g.seq));
+    g.first_tile = g.token * p.group / kPrefillRows + n - 1;
     shared = scalar_load(p.shared_lens + n - 1);
   }
-  first = bounded_seq(p, first);
-  if (first > seq) return SharedGroup{0, 0, 0};   // entries that fall
-  return SharedGroup{n - 1, first, whole_blocks(p, shared)};
+  if (g.seq > seq) return SharedGroup{0, 0, 0, 0, 0};   // entries that fall
+  g.group = n - 1;
+  g.shared = whole_blocks(p, shared);
+  return g;
 }
 
-// Tiles of 128 rows are numbered without a count of anybody's rows: group g, whose first row
-// is number r of all, begins with tile r / 128 + g. A group of n rows needs at most
-// n / 128 + 1 tiles (rounded down), so the next one's first is past its last.
 struct GroupRows {
   int seq;                // first sequence
   int token, token_end;   // rows of q
@@ -75,28 +98,31 @@ struct GroupRows {
 };
 __device__ __forceinline__ GroupRows group_of_tile(const SharedArgs& p, int t) {
   const int lane = threadIdx.x & 63;
-  GroupRows r;
+  GroupRows r{0, 0, 0, 0, 0};
   int n;
   if (p.num_groups <= 64) {
     const int at = min(lane, p.num_groups - 1);
     const int seq = bounded_seq(p, p.group_start[at]), end = bounded_seq(p, p.group_start[at + 1]), len = p.shared_lens[at];
-    const int token = token_of(p, seq), token_end = token_of(p, end);
-    n = __popcll(__ballot(lane < p.num_groups && token * p.group / kPrefillRows + lane <= t));
-    if (n < 1) return GroupRows{0, 0, 0, 0, 0};
+    const int token = token_of(p, seq), token_end = token_of(p, end), first = tiles_before(p, token, token_end);
+    // the last group that begins up to t and has rows
+    const uint64_t up_to = __ballot(lane < p.num_groups && first <= t && token < token_end);
+    if (up_to == 0) return r;
+    n = 64 - __builtin_clzll(up_to);
     r.seq = __builtin_amdgcn_readlane(seq, n - 1);
     r.token = __builtin_amdgcn_readlane(token, n - 1);
     r.token_end = __builtin_amdgcn_readlane(token_end, n - 1);
+    r.first_tile = __builtin_amdgcn_readlane(first, n - 1);
     r.shared = whole_blocks(p, __builtin_amdgcn_readlane(len, n - 1));
   } else {
     auto first_tile = [&](int g) { return token_of(p, bounded_seq(p, p.group_start[g])) * p.group / kPrefillRows + g; };
     n = count_up_to(p.num_groups, t, first_tile);
-    if (n < 1) return GroupRows{0, 0, 0, 0, 0};
+    if (n < 1) return r;
     r.seq = __builtin_amdgcn_readfirstlane(bounded_seq(p, p.group_start[n - 1]));
     r.token = __builtin_amdgcn_readfirstlane(token_of(p, r.seq));
     r.token_end = __builtin_amdgcn_readfirstlane(token_of(p, bounded_seq(p, p.group_start[n])));
+    r.first_tile = r.token * p.group / kPrefillRows + n - 1;
     r.shared = whole_blocks(p, scalar_load(p.shared_lens + n - 1));
   }
-  r.first_tile = r.token * p.group / kPrefillRows + n - 1;
   if (r.seq >= p.num_seqs || r.first_tile > t) r.token_end = r.token;   // entries that fall
   return r;
 }
@@ -182,13 +208,14 @@ __device__ __forceinline__ void add_parts(RowSums& r, int parts, const Load& loa
   if (parts - s >= 2) add_batch<2>(r, s, load), s += 2;
   if (parts - s >= 1) add_batch<1>(r, s, load);
 }
-// Adds the shared part of a row: head `head` of the key-value head's group, of token `token`
-// of the sequences' group; values d..d+3.
+// Adds the shared part of a row: head `head` of the key-value head's group, of row `token` of
+// q; values d..d+3.
 __device__ __forceinline__ void add_shared_parts(RowSums& r, const SharedArgs& p, const SharedGroup& g, int kv_head,
                                                  int token, int head, int d) {
   const int parts = (g.shared / kTokBlock + p.shared_split_blocks - 1) / p.shared_split_blocks;
-  const int row = max(0, token) * p.group + head;
-  const int t = token_of(p, g.seq) * p.group / kPrefillRows + g.group + row / kPrefillRows;
+  const int row = max(0, token - g.token) * p.group + head;
+  // (kept within the launch's tiles whatever the groups' entries hold)
+  const int t = min(g.first_tile + row / kPrefillRows, p.shared_row_tiles - 1);
   const int64_t first = ((int64_t)t * p.kv_heads + kv_head) * p.shared_splits * kPrefillRows + row % kPrefillRows;
   add_parts(r, parts, [&](int s, f32x4& y, float& m, float& l) {
     const int64_t at = first + s * kPrefillRows;

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(256) attn_join_one(SharedArgs p, int chunks) {
       m = ml[0];
       l = ml[1];
     });
-    add_shared_parts(sums, p, g, kv_head, seq - g.seq, in_group, d);
+    add_shared_parts(sums, p, g, kv_head, seq, in_group, d);
     typename F::T* dst = static_cast<typename F::T*>(p.out) + seq * p.o_ts + head * p.o_hs + d;
     *reinterpret_cast<u32x2*>(dst) = finish<F>(sums.o, sums.total, p.v_scale);
   }

@@ -13,7 +13,6 @@ __global__ void __launch_bounds__(256) attn_join_many(SharedArgs p, int chunks) 
   const RowTile rt = own_tile_of(p, tile);
   if (rt.rows <= 0) return;
   const SharedGroup g = group_of(p, rt.seq);
-  const int group_token = token_of(p, g.seq);
   const int quads = p.head_dim / 4;
   for (int x = chunk * 256 + threadIdx.x; x < rt.rows * quads; x += chunks * 256) {
     const int r = x / quads, d = 4 * (x - r * quads);
@@ -27,7 +26,7 @@ __global__ void __launch_bounds__(256) attn_join_many(SharedArgs p, int chunks) 
       l = ml[1];
     });
     const int row = rt.row0 + r, qi = divide(row, p.inv_group), head = row - qi * p.group;
-    add_shared_parts(sums, p, g, rt.kv_head, rt.q0 + qi - group_token, head, d);
+    add_shared_parts(sums, p, g, rt.kv_head, rt.q0 + qi, head, d);
     typename F::T* dst = static_cast<typename F::T*>(p.out) + (int64_t)(rt.q0 + qi) * p.o_ts +
                          (int64_t)(rt.kv_head * p.group + head) * p.o_hs + d;
     *reinterpret_cast<u32x2*>(dst) = finish<F>(sums.o, sums.total, p.v_scale);
