@@ -120,8 +120,12 @@ __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
   __shared__ int flag;
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int parts = p.chunks * p.splits, tile_no = blockIdx.x / (uint32_t)parts, rest = blockIdx.x - tile_no * parts;
-  const int split = rest / p.chunks, chunk = rest - split * p.chunks;
+  // parts of a tile stand side by side; workgroups of the same rows and values (chunks of
+  // ranks) are eight apart, on one XCD, whose cache they share
+  const uint32_t run = blockIdx.x / (8u * p.chunks), in_run = blockIdx.x - run * (8u * p.chunks);
+  const int chunk = in_run / 8, part_no = run * 8 + in_run % 8;
+  const int tile_no = part_no / p.splits, split = part_no - tile_no * p.splits;
+  if (tile_no >= (RB == 1 ? p.cap16 : p.cap64)) return;
   const LoraTile t = RB == 1 ? lora_tile(p, tile_no, p.tiles16, 2) : lora_tile(p, tile_no, p.tiles64, 3);
   if (t.rows <= 0 || t.adapter < 0) return;
   using T = typename F::T;
@@ -384,8 +388,6 @@ __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
 
   // ---- columns
   for (;;) {
-    const int done = col;
-    u32x4 o[RB][2];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       if (16 * b < t.rows) {
@@ -403,16 +405,17 @@ __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
           }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          o[b][x] = base[b][x];   // as it is without an adapter
+          u32x4 o = base[b][x];   // as it is without an adapter
           if (t.adapter >= 0) {
             const float factor = factors[b][c];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const f32x4 v = acc[2 * x + i / 2];
-              o[b][x][i] = F::pack(F::lo(base[b][x][i]) + factor * v[2 * (i % 2)],
-                                   F::hi(base[b][x][i]) + factor * v[2 * (i % 2) + 1]);
+              o[i] = F::pack(F::lo(base[b][x][i]) + factor * v[2 * (i % 2)], F::hi(base[b][x][i]) + factor * v[2 * (i % 2) + 1]);
             }
           }
+          if (16 * b + c < t.rows && col + 32 * x + 8 * h < col_end)
+            *reinterpret_cast<u32x4*>(out_row[b] + col + 32 * x) = o;
         }
       }
     }
@@ -422,12 +425,6 @@ __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
       load_base(col);
       load_b(col);
     }
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (16 * b + c < t.rows && done + 32 * x + 8 * h < col_end)
-          *reinterpret_cast<u32x4*>(out_row[b] + done + 32 * x) = o[b][x];
     if (!more) break;
   }
 }
@@ -436,6 +433,7 @@ template <class F, int RB>
 void shrink_tiles(const LoraArgs& a, int chunk_tiles, dim3 grid, hipStream_t s) {
   if (chunk_tiles == 1) hipLaunchKernelGGL((lora_shrink<F, RB, 1>), grid, dim3(256), 0, s, a);
   else if (chunk_tiles == 2) hipLaunchKernelGGL((lora_shrink<F, RB, 2>), grid, dim3(256), 0, s, a);
+  else if (chunk_tiles == 3) hipLaunchKernelGGL((lora_shrink<F, RB, 3>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((lora_shrink<F, RB, 4>), grid, dim3(256), 0, s, a);
 }
 
@@ -463,7 +461,7 @@ hipError_t launch_lora_plan(const LoraPlanArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& a, bool bf16, int chunk_tiles, hipStream_t s) {
-  const dim3 grid((unsigned)((a.tall_a ? a.cap64 : a.cap16) * a.chunks * a.splits));
+  const dim3 grid((unsigned)(((a.tall_a ? a.cap64 : a.cap16) * a.splits + 7) / 8 * 8 * a.chunks));
   if (a.tall_a) bf16 ? shrink_tiles<BF16, 4>(a, chunk_tiles, grid, s) : shrink_tiles<F16, 4>(a, chunk_tiles, grid, s);
   else bf16 ? shrink_tiles<BF16, 1>(a, chunk_tiles, grid, s) : shrink_tiles<F16, 1>(a, chunk_tiles, grid, s);
   return hipGetLastError();

@@ -64,8 +64,8 @@ qg::LoraDecomposition decompose(int64_t tokens, int64_t adapters, int64_t K, int
   const int64_t cap = d.tall_a ? l.cap64 : l.cap16;
   d.rank_tiles = (rank + qg::kLoraRankTile - 1) / qg::kLoraRankTile;
   const int64_t tiles = (int64_t)slices * d.rank_tiles;
-  d.chunk_tiles = tiles >= 3 ? 4 : (int)tiles;
-  d.chunks = (int)((tiles + d.chunk_tiles - 1) / d.chunk_tiles);
+  d.chunks = (int)((tiles + 3) / 4);   // of up to four tiles, whose sums stay in registers
+  d.chunk_tiles = (int)((tiles + d.chunks - 1) / d.chunks);
   // Parts of K: up to two workgroups per compute unit, which are resident at once, each of
   // whole units of K (a run of steps for each of its four waves). 64 rows of 64 adapters, 48
   // ranks on 8192: in 8 parts 13.6 us, in 4 13.8, in 6 uneven ones 17.1, in 16 20. More tiles
