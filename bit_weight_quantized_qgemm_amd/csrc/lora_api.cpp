@@ -66,14 +66,31 @@ qg::LoraDecomposition decompose(int64_t tokens, int64_t adapters, int64_t K, int
   const int64_t tiles = (int64_t)slices * d.rank_tiles;
   d.chunks = (int)((tiles + 3) / 4);   // of up to four tiles, whose sums stay in registers
   d.chunk_tiles = (int)((tiles + d.chunks - 1) / d.chunks);
-  // Parts of K: up to two workgroups per compute unit, which are resident at once, each of
-  // whole units of K (a run of steps for each of its four waves). 64 rows of 64 adapters, 48
-  // ranks on 8192: in 8 parts 13.6 us, in 4 13.8, in 6 uneven ones 17.1, in 16 20. More tiles
-  // than the workspace has counters fill the device without a split.
-  const int64_t unit = d.tall_a ? 256 : 512, units = (K + unit - 1) / unit;
-  int64_t want = std::max<int64_t>(1, 2 * qg::device_cu_count() / std::max<int64_t>(1, cap * d.chunks));
-  if (cap * d.chunks > qg::kMaxCounters) want = 1;
-  d.split_k = (int)((units + want - 1) / want * unit);
+  // Parts of K, in whole units (a run of steps for each of a workgroup's four waves).
+  //  - Tiles of 16 rows: up to two workgroups per compute unit, of equal length (48 ranks on
+  //    8192, us: 64 rows of 64 adapters in 4 parts 12.9, 6 14.7, 8 12.2, 16 16.7; 256 rows of 60
+  //    in 4, 6, 8 12.9, 15.4, 12.6; 128 rows of 24 at rank 64 in 4 13.9, 8 9.6, 16 10.8).
+  //  - Tiles of 64 rows: the fewest turns of the units, a turn counting its length and one
+  //    more (8192 rows of 8192, rank 16: 134 tiles in 1, 2, 3, 4, 5 parts 47, 57, 41, 49, 43;
+  //    of 4096 at 96 ranks, 266 in 1, 2, 4, 6: 55, 47, 45, 50; 2048 of 8192 at rank 32, 38 in
+  //    1, 4, 6, 8: 46, 17.5, 15.3, 17.9).
+  // More tiles than the workspace has counters fill the device without parts.
+  const int64_t unit = d.tall_a ? 256 : 512, units = (K + unit - 1) / unit, cus = qg::device_cu_count();
+  int64_t per = units;   // units of a part
+  if (cap * d.chunks > qg::kMaxCounters) {
+  } else if (d.tall_a) {
+    int64_t least = INT64_MAX;
+    for (int64_t s = 1; s <= std::min<int64_t>(units, 8); ++s) {
+      const int64_t each = (units + s - 1) / s, cost = (cap * d.chunks * s + cus - 1) / cus * (each + 1);
+      if (cost < least) least = cost, per = each;
+    }
+  } else {
+    const int64_t want = std::max<int64_t>(1, 2 * cus / std::max<int64_t>(1, cap * d.chunks));
+    const int64_t fewest = (units + want - 1) / want;
+    per = fewest;
+    while (units % per != 0 && per < 2 * fewest) ++per;
+  }
+  d.split_k = (int)(per * unit);
   d.splits = (int)((K + d.split_k - 1) / d.split_k);
   d.y_offset = qg::kCounterBytes;
   d.partial_offset = d.y_offset + qg::align256((size_t)tokens * tiles * 16 * 4);
