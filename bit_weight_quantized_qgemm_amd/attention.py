@@ -61,6 +61,7 @@ class KVCache:
         torch = _torch()
         self._int32_type, self._float32_type = torch.int32, torch.float32
         self._empty_like, self._stream = torch.empty_like, torch._C._cuda_getCurrentRawStream
+        self._current = torch._C._cuda_getDevice
         self._acts = {torch.float16: DT_F16, torch.bfloat16: DT_BF16}
         self._norm_shape = torch.Size((k.shape[3],))
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
@@ -325,6 +326,10 @@ def attn_decode_shared(q, cache: KVCache, block_table, seq_lens, max_len: int, g
     and are read and computed once for all of them. group_start int32 [groups + 1], nondecreasing, and shared_lens int32
     [groups] on the device; sequences outside all groups share nothing. max_shared bounds shared_lens (a host number: more
     is taken as max_shared). Keys and values of shared tokens have to be finite."""
+    if cache._current() != cache._index:
+        with _torch().cuda.device(cache._index):
+            return attn_decode_shared(q, cache, block_table, seq_lens, max_len, group_start, shared_lens, max_shared, scale, window,
+                                      sinks, out, workspace)
     shape, dt, out, qa, oa = _queries(q, cache, out)
     B, H, D = shape
     table, cols, seqs = _table(block_table, cache)
@@ -351,6 +356,10 @@ def attn_prefill_shared(q, cache: KVCache, block_table, q_start, seq_lens, max_q
                         out=None, workspace: Workspace | None = None):
     """``attn_prefill`` for a batch whose sequences begin with the same tokens, group by group; the groups as in
     ``attn_decode_shared``. New tokens may be among the shared ones."""
+    if cache._current() != cache._index:
+        with _torch().cuda.device(cache._index):
+            return attn_prefill_shared(q, cache, block_table, q_start, seq_lens, max_q, max_len, group_start, shared_lens, max_shared,
+                                       scale, window, sinks, out, workspace)
     shape, dt, out, qa, oa = _queries(q, cache, out)
     T, H, D = shape
     table, cols, seqs = _table(block_table, cache)

@@ -222,13 +222,14 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
   if (rt.rows <= 0 || split >= rt.parts) return;
 
   // ---- kShared: positions of this lane's row and of the wave's
-  int shared_pos = -1, shared_min = INT32_MAX, shared_max = -1;
+  constexpr int kFar = INT32_MAX / 2;   // past every position
+  int shared_pos = -1, shared_min = kFar, shared_max = -1;
   if constexpr (MODE == kShared) {
     const int first = rt.row0 + wave * 32, r = first + c, end = rt.row0 + rt.rows;
     if (first < end)
       shared_pos = position_of(p, rt.seq, rt.q0, min(r, end - 1), first, min(first + 31, end - 1));
     if (r >= end) shared_pos = -1;
-    shared_min = r < end ? shared_pos : INT32_MAX;
+    shared_min = r < end ? shared_pos : kFar;
     shared_max = shared_pos;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {

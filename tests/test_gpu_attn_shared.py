@@ -138,12 +138,84 @@ def test_prefill(new, lens, groups, before, H, KV, D, act, cache, page, layout, 
 def test_many_groups():
     _say("many groups")
     rng = np.random.default_rng(5)
-    # more than 64 groups, and more than 64 * 64 sequences in none of them
+    # more than 64 groups
     lens = [20 + i % 7 for i in range(200)]
     pg = SharedPaged(rng, lens, [(i % 4, 1, 16) for i in range(120)], 1, 32, "f16", 16, DEV, before=5)
     _decode(rng, pg, 2, "f16")
     new = [1 + i % 3 for i in range(200)]
     _prefill(rng, pg, new, 2, "f16")
+
+
+def test_thousands_of_groups():
+    """More groups than one look at 64 x 64 of them finds, and more than one run of lanes holds."""
+    _say("thousands of groups")
+    rng = np.random.default_rng(20)
+    n = 4500
+    pg = SharedPaged(rng, [17 + i % 3 for i in range(2 * n)], [(2, 1, 16)] * n, 1, 16, "f16", 16, DEV)
+    _decode(rng, pg, 1, "f16")
+    _prefill(rng, pg, [1] * (2 * n), 1, "f16")
+
+
+LONG = [
+    # shared and own runs of more pages than a wave holds the places of; lost pages in both
+    ([2400, 3700, 2110, 2200], [(3, 132, 2112)], 4, 2, 128, "f16", "f16", 16, [(0, 70, -1), (1, 70, -1), (2, 70, -1), (1, 200, -1)]),
+    ([2400, 3700, 2110, 2200], [(3, 132, 2112)], 4, 2, 64, "bf16", "fp8", 16, []),
+    ([2400, 3700, 1500, 2200], [(3, 33, 2112)], 2, 1, 96, "bf16", "bf16", 64, [(3, 20, 5)]),
+    ([1300, 1700, 1110], [(3, 66, 1056)], 2, 1, 256, "f16", "f16", 16, [(0, 40, -1), (1, 40, -1), (2, 40, -1)]),
+]
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("lens,groups,H,KV,D,act,cache,page,missing", LONG)
+def test_long_runs(lens, groups, H, KV, D, act, cache, page, missing, splits):
+    _say("long", lens, groups, H, KV, D, act, cache, page, missing, splits)
+    rng = np.random.default_rng(D)
+    scales = (2.0 ** -4, 2.0 ** -3) if cache == "fp8" else (1.0, 1.0)
+    pg = SharedPaged(rng, lens, groups, KV, D, cache, page, DEV, scales=scales, missing=missing)
+    qg.set_attn_splits(splits)
+    for window, sinks in ((0, 0), (1500, 5)):
+        _decode(rng, pg, H, act, window, sinks, what=(lens, splits))
+        _prefill(rng, pg, [3, 40, 7, 1][:len(lens)], H, act, window, sinks, what=(lens, splits))
+
+
+def test_rows_of_q_before_the_first_sequence():
+    _say("offset rows")
+    rng = np.random.default_rng(21)
+    pg = SharedPaged(rng, [90, 80, 70], [(3, 4, 64)], 2, 64, "f16", 16, DEV)
+    bits, q = _values(rng, (12, 4, 64), "f16")
+    start = torch.tensor([3, 5, 5, 9], dtype=torch.int32, device=DEV)
+    out = torch.full((12, 4, 64), 7.0, dtype=torch.float16, device=DEV)
+    for splits in (1, 3):
+        qg.set_attn_splits(splits)
+        out.fill_(7.0)
+        qg.attn_prefill_shared(to_torch(bits, "f16", DEV), pg.cache, pg.table_dev, start, pg.lens_dev, 4, 90, pg.group_start,
+                               pg.shared_lens, 64, out=out)
+        torch.cuda.synchronize()
+        rows = [(0, 3, 88), (0, 4, 89)] + [(2, 5 + i, 66 + i) for i in range(4)]
+        refs = [pg.attend(b, q[t], pos, 0.125) for b, t, pos in rows]
+        check(oa.decode(to_bits(out), "f16")[[t for _, t, _ in rows]], refs, "f16", PREFILL_WEIGHTS["f16"], "offset")
+        assert bool((out[:3] == 7.0).all()) and bool((out[9:] == 7.0).all())
+
+
+def test_calls_on_two_streams_at_once():
+    _say("two streams")
+    rng = np.random.default_rng(22)
+    pg = SharedPaged(rng, [700, 650, 660, 800], [(4, 32, 512)], 2, 128, "f16", 16, DEV)
+    qs = [to_torch(_values(rng, (4, 8, 128), "f16")[0], "f16", DEV) for _ in range(2)]
+
+    def call(q):
+        return qg.attn_decode_shared(q, pg.cache, pg.table_dev, pg.lens_dev, 800, pg.group_start, pg.shared_lens, 512)
+
+    want = [call(q) for q in qs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call(qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
 
 
 @pytest.mark.parametrize("max_shared", [0, 15, 16, 40, 64, 1000])

@@ -75,6 +75,24 @@ def test_the_change_to_tall_tiles(T):
     _run(rng, T, 64, [64], 16, 300, "f16", "own")
 
 
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,rank", [(769, 40), (800, 64), (1025, 16), (1100, 72), (1030, 128), (1040, 136), (1025, 256),
+                                    (2561, 8), (2600, 32), (2700, 24)])
+def test_tall_tiles(T, rank, fmt):
+    """Tiles of 64 rows in the first product, the second, and both; the last ones part empty."""
+    rng = np.random.default_rng(T + rank)
+    _run(rng, T, 104, [72, 136], rank, 5, fmt, "sorted", gap=8)
+
+
+def test_tall_tiles_of_many_kinds():
+    rng = np.random.default_rng(77)
+    _run(rng, 1200, 64, [64], 64, 7, "bf16", "mixed", ranks=[64, 8, 0, 17, 33, 64, 1])
+    _run(rng, 2600, 32, [16, 40], 16, 900, "f16", "mixed")
+    _run(rng, 1300, 2056, [24], 48, 3, "f16", "one")
+    _run(rng, 2570, 1032, [8] * 8, 8, 4, "bf16", "none")
+    _run(rng, 1500, 40, [32, 32, 32, 32, 32, 32, 32, 32], 40, 6, "f16", "own", with_base=False)
+
+
 @pytest.mark.parametrize("K", [8, 24, 32, 40, 120, 128, 136, 1000, 2056, 4096])
 def test_inner_lengths(K):
     rng = np.random.default_rng(K)
@@ -138,7 +156,7 @@ def test_products_beyond_16_bits(fmt, a_dev, b_dev):
 
 def test_in_place_equals_out_of_place():
     rng = np.random.default_rng(4)
-    for T in (13, 300):
+    for T in (13, 300, 2600):
         p, ids, (_, xd), (base_bits, bd), od = _run(rng, T, 128, [64, 72], 16, 4, "f16", "mixed")
         y, buf = guarded(T, p.N, "f16", DEV, 16, base_bits)
         assert qg.lora(xd, p.adapters, _batch(ids, 4), base=y, out=y) is y
@@ -164,7 +182,7 @@ def test_rows_without_an_adapter_keep_every_bit_of_their_base():
 
 def test_rows_do_not_influence_each_other():
     rng = np.random.default_rng(6)
-    for T in (24, 330):
+    for T in (24, 330, 2700):
         p = Pool(rng, 3, 192, [136], 24, "bf16", DEV)
         ids = rng.integers(-1, 3, T)
         x_bits, _ = values(rng, (T, 192), "bf16")
@@ -187,7 +205,7 @@ def test_other_adapters_are_not_read():
     p = Pool(rng, 4, 64, [64], 16, "f16", DEV, gap=8)
     p.adapters.a[2].fill_(float("nan"))
     p.adapters.b[2].fill_(float("nan"))
-    for T in (12, 280):
+    for T in (12, 280, 2590):
         ids = rng.choice([0, 1, 3, -1], T)
         x_bits, x = values(rng, (T, 64), "f16")
         out = qg.lora(to_torch(x_bits, "f16", DEV), p.adapters, _batch(ids, 4))
@@ -250,6 +268,37 @@ def test_another_stream():
         got = qg.lora(x, p.adapters, _batch(ids, 3))
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_calls_on_two_streams_at_once():
+    """One batch and pool in two streams, whose calls overlap: each stream has a workspace of its own."""
+    rng = np.random.default_rng(15)
+    p = Pool(rng, 6, 4096, [2048], 16, "f16", DEV)
+    ids = rng.integers(-1, 6, 96)
+    xs = [to_torch(values(rng, (96, 4096), "f16")[0], "f16", DEV) for _ in range(2)]
+    batch = _batch(ids, 6)
+    want = [qg.lora(x, p.adapters, batch) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(qg.lora(xs[i], p.adapters, batch))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_one_row_against_every_adapter_of_a_batch():
+    """The same row and adapter many times give the same bits wherever they stand."""
+    rng = np.random.default_rng(16)
+    p = Pool(rng, 3, 320, [200], 24, "bf16", DEV)
+    for T in (37, 1290):
+        row, _ = values(rng, (1, 320), "bf16")
+        out = to_bits(qg.lora(to_torch(np.repeat(row, T, axis=0), "bf16", DEV), p.adapters, _batch(np.arange(T) % 3, 3)))
+        for i in range(3):
+            assert (out[i::3] == out[i]).all()
 
 
 def test_empty_batches():
