@@ -302,9 +302,11 @@ qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, 
     double own_cost, plain_cost;
     if (prefill) {
       const int64_t plain_blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), mask);
-      prefill_parts(pl.own.tiles, pl.own.part_rows, plain_blocks, head_dim, true, 1, &plain_cost);
+      // tiles that can hold rows: where few of the sequences are long, most of max_q's do not
+      const int64_t own_live = std::min(pl.own.tiles, (rows / pl.own.part_rows + num_seqs) * kv_heads);
+      prefill_parts(own_live, pl.own.part_rows, plain_blocks, head_dim, true, 1, &plain_cost);
       const int64_t own_turns = (own_len + 16 * step - 1) / (16 * step);
-      own_cost = (head_dim <= 64 ? 0.65 : 1.15) * own_turns * (double)pl.own.tiles / cus;
+      own_cost = (head_dim <= 64 ? 0.65 : 1.15) * own_turns * (double)own_live / cus;
       cost = 2 * live <= cus ? turn * ((turns + parts - 1) / parts) : cost;
       cost += own_cost;
     } else {
@@ -337,13 +339,14 @@ qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, 
     return pl;
   }
   size_t end = qg::kCounterBytes;
-  const size_t own_rows = (size_t)pl.own.tiles * pl.own.splits * pl.own.part_rows;
+  const size_t all_rows = (size_t)num_tokens * q_heads;
+  const size_t own_rows = prefill ? all_rows * pl.own.splits : (size_t)pl.own.tiles * pl.own.splits * pl.own.part_rows;
   pl.own.stats_offset = end;
   pl.own.partial_offset = end + qg::align256(own_rows * 8);
   end = pl.own.partial_offset + qg::align256(own_rows * head_dim * 4);
-  const size_t shared_rows = (size_t)pl.tiles * pl.splits * qg::kPrefillRows;
+  const size_t shared_rows = all_rows * pl.splits;
   pl.stats_offset = end;
-  pl.partial_offset = end + shared_rows * 8;
+  pl.partial_offset = end + qg::align256(shared_rows * 8);
   pl.ws_bytes = pl.partial_offset + shared_rows * head_dim * 4;
   return pl;
 }

@@ -55,6 +55,7 @@ struct AttnArgs {
   const int32_t* lens;
   const int32_t* q_start;   // prefill
   float* partial;           // [tile][split][part_rows][head_dim], sums before the division
+                            // (own tokens beside shared ones, many-token calls: as shared_partial)
   float* stats;             // [tile][split][part_rows] (maximum in log2 units, sum of weights)
   uint32_t* counters;       // decode: one per tile, zero between calls
   int32_t num_seqs, kv_heads, group, head_dim;
@@ -75,8 +76,8 @@ struct AttnArgs {
 struct SharedArgs : AttnArgs {
   const int32_t* group_start;
   const int32_t* shared_lens;
-  float* shared_partial;    // [shared tile][shared split][kPrefillRows][head_dim]
-  float* shared_stats;      // [shared tile][shared split][kPrefillRows] (maximum, sum)
+  float* shared_partial;    // [shared split][kv head][token][head of it][head_dim]
+  float* shared_stats;      // [shared split][kv head][token][head of it] (maximum, sum)
   int32_t num_groups, max_shared;
   int32_t shared_row_tiles; // tiles of 128 rows of a group, for each key-value head
   int32_t shared_splits;

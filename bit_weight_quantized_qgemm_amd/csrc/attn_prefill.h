@@ -163,7 +163,7 @@ __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& p, int tile) {
 // The same tile without the tokens that its sequence shares.
 __device__ __forceinline__ RowTile own_tile_of(const SharedArgs& p, int tile) {
   RowTile rt = row_tile_of(p, tile);
-  const OwnBlocks own = own_blocks(rt.see, group_of(p, rt.seq).shared, p.splits, p.split_step);
+  const OwnBlocks own = own_blocks(rt.see, shared_tokens(p, rt.seq), p.splits, p.split_step);
   rt.v_first = own.first;
   rt.split_blocks = own.split_blocks;
   rt.parts = own.parts;
@@ -641,12 +641,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
   }
   int64_t r;
   float *partial = p.partial, *stats = p.stats;
+  if constexpr (MODE == kAlone) r = ((int64_t)tile * p.splits + split) * p.part_rows + row - rt.row0;
+  else r = part_place(p, split, rt.kv_head, rt.q0 * p.group + row);
   if constexpr (MODE == kShared) {
-    r = ((int64_t)tile * p.shared_splits + split) * kPrefillRows + row - rt.row0;
     partial = p.shared_partial;
     stats = p.shared_stats;
-  } else {
-    r = ((int64_t)tile * p.splits + split) * p.part_rows + row - rt.row0;
   }
   float* dst = partial + r * p.head_dim;
 #pragma unroll

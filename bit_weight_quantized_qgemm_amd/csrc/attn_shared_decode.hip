@@ -11,9 +11,9 @@ __global__ void __launch_bounds__(256) attn_join_one(SharedArgs p, int chunks) {
   const uint32_t block = blockIdx.x + p.first_block;
   const int seq = (int)(block / (uint32_t)chunks), chunk = (int)(block - (uint32_t)seq * (uint32_t)chunks);
   const int len = min(max(scalar_load(p.lens + seq), 0), p.max_len);
-  const SharedGroup g = group_of(p, seq);
+  const int shared = shared_tokens(p, seq);
   const Visible see(len, p.window ? len - p.window : 0, p.window ? p.sinks : 0);
-  const OwnBlocks own = own_blocks(see, g.shared, p.splits, p.split_step);
+  const OwnBlocks own = own_blocks(see, shared, p.splits, p.split_step);
   const int quads = p.head_dim / 4, all = p.kv_heads * p.group * quads;
   for (int x = chunk * 256 + threadIdx.x; x < all; x += chunks * 256) {
     const int head = x / quads, d = 4 * (x - head * quads);
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(256) attn_join_one(SharedArgs p, int chunks) {
       m = ml[0];
       l = ml[1];
     });
-    add_shared_parts(sums, p, g, kv_head, seq, in_group, d);
+    add_shared_parts(sums, p, shared, kv_head, seq * p.group + in_group, d);
     typename F::T* dst = static_cast<typename F::T*>(p.out) + seq * p.o_ts + head * p.o_hs + d;
     *reinterpret_cast<u32x2*>(dst) = finish<F>(sums.o, sums.total, p.v_scale);
   }

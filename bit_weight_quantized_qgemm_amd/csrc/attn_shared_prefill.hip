@@ -12,23 +12,22 @@ __global__ void __launch_bounds__(256) attn_join_many(SharedArgs p, int chunks) 
   const int tile = (int)(block / (uint32_t)chunks), chunk = (int)(block - (uint32_t)tile * (uint32_t)chunks);
   const RowTile rt = own_tile_of(p, tile);
   if (rt.rows <= 0) return;
-  const SharedGroup g = group_of(p, rt.seq);
+  const int shared = shared_tokens(p, rt.seq);
   const int quads = p.head_dim / 4;
   for (int x = chunk * 256 + threadIdx.x; x < rt.rows * quads; x += chunks * 256) {
     const int r = x / quads, d = 4 * (x - r * quads);
     RowSums sums;
-    const int64_t first = (int64_t)tile * p.splits * p.part_rows + r;
+    const int row = rt.row0 + r, qi = divide(row, p.inv_group), token = rt.q0 + qi;
+    const int head = rt.kv_head * p.group + row - qi * p.group;
     add_parts(sums, rt.parts, [&](int s, f32x4& y, float& m, float& l) {
-      const int64_t at = first + (int64_t)s * p.part_rows;
+      const int64_t at = part_place(p, s, rt.kv_head, rt.q0 * p.group + row);
       y = *reinterpret_cast<const f32x4*>(p.partial + at * p.head_dim + d);
       const f32x2 ml = *reinterpret_cast<const f32x2*>(p.stats + 2 * at);
       m = ml[0];
       l = ml[1];
     });
-    const int row = rt.row0 + r, qi = divide(row, p.inv_group), head = row - qi * p.group;
-    add_shared_parts(sums, p, g, rt.kv_head, rt.q0 + qi, head, d);
-    typename F::T* dst = static_cast<typename F::T*>(p.out) + (int64_t)(rt.q0 + qi) * p.o_ts +
-                         (int64_t)(rt.kv_head * p.group + head) * p.o_hs + d;
+    add_shared_parts(sums, p, shared, rt.kv_head, rt.q0 * p.group + row, d);
+    typename F::T* dst = static_cast<typename F::T*>(p.out) + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d;
     *reinterpret_cast<u32x2*>(dst) = finish<F>(sums.o, sums.total, p.v_scale);
   }
 }

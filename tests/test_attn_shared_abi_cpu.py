@@ -90,10 +90,9 @@ def test_null_struct_and_modes():
     (4, 1, 768, 898, 32, 32, 128, 5), (64, 1, 8192, 8704, 64, 8, 128, 1), (101, 4, 4096, 4800, 32, 8, 128, 3),
     (1, 1, 16, 16, 1, 1, 16, 1), (300, 150, 1 << 20, 1 << 24, 128, 1, 256, 40), (65535, 65535, 64, 128, 8, 8, 64, 1)])
 def test_workspaces_hold_every_part(seqs, groups, max_shared, max_len, H, KV, D, new, splits, window, sinks):
-    """Counters; for each row tile of the shared rows at least one part of statistics and sums, all parts in whole tiles
-    of 128; the plain call's own parts."""
+    """Counters; statistics and sums of every row (token and head) for each part of the shared tokens, all parts of whole
+    tiles of keys, and for at least one part of the own ones; the plain call's own parts."""
     qg.set_attn_splits(splits)
-    group = H // KV
     for prefill in (False, True):
         tokens = seqs * new if prefill else seqs
         if tokens > 1 << 20:
@@ -101,16 +100,12 @@ def test_workspaces_hold_every_part(seqs, groups, max_shared, max_len, H, KV, D,
         args = (seqs, tokens, new, max_len) if prefill else (seqs, max_len)
         size = qg.attn_prefill_shared_workspace_bytes if prefill else qg.attn_decode_shared_workspace_bytes
         got = size(*args, H, KV, D, window, sinks, groups, max_shared)
-        tiles = (tokens * group // 128 + groups) * KV
-        one = 128 * (D + 2) * 4
-        parts = min(splits or 1, max_shared // 16)
         blocks = max_shared // 16
+        parts = min(splits or 1, blocks)
         step = 4 if D <= 128 else 2
         per = -(-(-(-blocks // parts)) // step) * step
         parts = -(-blocks // per)
-        own_rows = min(new * group, 128) if prefill else min(group, 16)
-        own_tiles = seqs * KV * (-(-new * group // 128) if prefill else -(-group // 16))
-        least = 65536 + tiles * parts * one + (own_tiles * own_rows * (D + 2) * 4 if prefill else 0)
+        least = 65536 + tokens * H * (parts + 1) * (D + 2) * 4
         assert got >= least
         assert qg.lib().qgemm_attn_set_sharing(2) == OK
         plain = size(*args, H, KV, D, window, sinks, groups, max_shared)
@@ -118,6 +113,22 @@ def test_workspaces_hold_every_part(seqs, groups, max_shared, max_len, H, KV, D,
                    qg.attn_decode_workspace_bytes(seqs, max_len, H, KV, D, window, sinks))
         assert plain == without
         qg.set_attn_sharing(1)
+
+
+@pytest.mark.parametrize("seqs,new,max_len,max_shared", [(32, 4096, 12400, 8192), (64, 8192, 40000, 32000),
+                                                         (1000, 4096, 70000, 65536), (500, 1, 9000, 8192)])
+@pytest.mark.parametrize("mode", [0, 1], ids=["automatic", "shared"])
+def test_one_long_prompt_among_single_tokens(mode, seqs, new, max_len, max_shared):
+    """Memory goes by the rows that there are, not by the longest prompt times the sequences, nor by tiles of groups with few
+    rows: one place per row, with sums and statistics, in each of at most 64 parts (of 256 workgroups' worth of tiles) of the
+    shared and as many of the own tokens."""
+    H, KV, D, tokens = 64, 8, 128, seqs - 1 + new
+    qg.set_attn_sharing(mode)
+    got = qg.attn_prefill_shared_workspace_bytes(seqs, tokens, new, max_len, H, KV, D, 0, 0, seqs // 2, max_shared)
+    one = tokens * H * (D + 2) * 4
+    tiles = (seqs // 2 + tokens * H // KV // 128) * KV
+    parts = max(1, -(-8 * 256 // tiles))
+    assert got <= 65536 + 4 * 256 + 2 * parts * one
 
 
 def test_small_workspaces_are_refused():

@@ -178,6 +178,21 @@ def test_long_runs(lens, groups, H, KV, D, act, cache, page, missing, splits):
         _prefill(rng, pg, [3, 40, 7, 1][:len(lens)], H, act, window, sinks, what=(lens, splits))
 
 
+@pytest.mark.parametrize("sharing", [0, 1])
+@pytest.mark.parametrize("splits", [0, 2])
+def test_one_long_prompt_among_single_tokens(splits, sharing):
+    """Most of the tiles that max_q allows hold no row."""
+    _say("long prompt among single tokens", splits, sharing)
+    rng = np.random.default_rng(53)
+    qg.set_attn_splits(splits)
+    qg.set_attn_sharing(sharing)
+    new = [1, 0, 1, 150, 1, 1, 2, 1, 1]
+    lens = [260 + 3 * i for i in range(9)]
+    lens[3] = 430
+    pg = SharedPaged(rng, lens, [(5, 16, 256), (2, 8, 128)], 2, 64, "f16", 16, DEV, before=1)
+    _prefill(rng, pg, new, 8, "f16")
+
+
 def test_rows_of_q_before_the_first_sequence():
     _say("offset rows")
     rng = np.random.default_rng(21)
