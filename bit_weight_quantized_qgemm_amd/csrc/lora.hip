@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
         for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[s][x][e]));
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // 2^e <= top < 2^(e+1) for normal values; an infinite or NaN sum stays what it is
+    // 2^e <= top < 2^(e+1) for normal values; an infinite or NaN sum stays what it is, the
+    // rest of an infinite one is 0
     const int e = min(max((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127, -100), 100);
     const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
     if (h == 0) factors[b][c] = (p.scales ? p.scales[t.adapter] : 1.f) * __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
@@ -378,7 +379,8 @@ __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
         for (int i = 0; i < 2; ++i) {
           const float v0 = v[s][x][2 * i] * down, v1 = v[s][x][2 * i + 1] * down;
           hi[2 * x + i] = F::pack(v0, v1);
-          lo[2 * x + i] = F::pack(v0 - F::lo(hi[2 * x + i]), v1 - F::hi(hi[2 * x + i]));
+          const float h0 = F::lo(hi[2 * x + i]), h1 = F::hi(hi[2 * x + i]);
+          lo[2 * x + i] = F::pack(isinf(h0) ? 0.f : v0 - h0, isinf(h1) ? 0.f : v1 - h1);
         }
       if constexpr (PAIRED) {
         terms[b][s][0][lane] = h >= eights ? lo : hi;

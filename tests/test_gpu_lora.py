@@ -200,6 +200,27 @@ def test_rows_do_not_influence_each_other():
         assert np.array_equal(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("T", [3, 1100])
+@pytest.mark.parametrize("rank", [8, 16, 24, 72])
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+def test_infinite_sums_stay_infinite(T, rank, fmt):
+    """Where every term of a sum has one sign the formula gives an infinity, not NaN; zeros times it give NaN."""
+    _say("infinite", T, rank, fmt)
+    dtype = torch.float16 if fmt == "f16" else torch.bfloat16
+    K, N = 72, 24
+    x = torch.ones(T, K, dtype=dtype, device=DEV)
+    x[0, 3], x[2, 5] = float("inf"), -float("inf")
+    a = torch.full((1, rank, K), 0.5, dtype=dtype, device=DEV)
+    b = torch.full((1, N, rank), 0.25, dtype=dtype, device=DEV)
+    b[0, 1::3], b[0, 2::3] = -0.25, 0.0
+    out = qg.lora(x, qg.LoraAdapters(a, b), _batch(np.zeros(T, np.int64), 1)).float().cpu()
+    part = K * 0.5 * 0.25 * rank   # exact in both formats
+    ref = torch.tensor([part, -part, 0.0]).repeat(N // 3).expand(T, N).clone()
+    ref[0] = torch.tensor([float("inf"), -float("inf"), float("nan")]).repeat(N // 3)
+    ref[2] = torch.tensor([-float("inf"), float("inf"), float("nan")]).repeat(N // 3)
+    assert torch.equal(torch.nan_to_num(out, nan=123.0), torch.nan_to_num(ref, nan=123.0))
+
+
 def test_other_adapters_are_not_read():
     rng = np.random.default_rng(7)
     p = Pool(rng, 4, 64, [64], 16, "f16", DEV, gap=8)
