@@ -353,60 +353,60 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<OWN, Shared
     if (h == 0) *reinterpret_cast<f32x2*>(p.stats + (part_id * p.part_rows + c) * 2) = f32x2{mref, sum};
     return;
   } else {
-  // ---- join the waves
-  auto& part = lds->part;
-  auto &part_max = lds->part_max, &part_sum = lds->part_sum;
-  if (lane < kDecodeRows) {
-    part_max[wave][lane] = mref;
-    part_sum[wave][lane] = sum;
-  }
-  if (c < rows) {
-#pragma unroll
-    for (int j = 0; j < S::kVCols; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < S::kVDims; i += 4)
-          *reinterpret_cast<f32x4*>(&part[wave][c][j * 16 * S::kVDims + (4 * h + r) * S::kVDims + i]) =
-              f32x4{acc[j][i][r], acc[j][i + 1][r], acc[j][i + 2][r], acc[j][i + 3][r]};
-  }
-  __syncthreads();
-
-  const int quads = p.head_dim / 4;   // fp32 quadruples of a row
-  float* stats = p.stats + part_id * p.part_rows * 2;
-  const rsrc_t out_r = make_rsrc(p.partial + part_id * p.part_rows * p.head_dim, (uint32_t)(p.part_rows * p.head_dim * 4));
-  for (int x = threadIdx.x; x < rows * quads; x += 256) {
-    const int row = EXACT ? x / (DP / 4) : x / quads, d = 4 * (x - row * quads);
-    float m = part_max[0][row];
-#pragma unroll
-    for (int w = 1; w < kDecodeWaves; ++w) m = fmaxf(m, part_max[w][row]);
-    const float base = m == kNegInf ? 0.f : m;
-    float total = 0.f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kDecodeWaves; ++w) {
-      const float f = exp2_of(part_max[w][row] - base);
-      total += f * part_sum[w][row];
-      const f32x4 y = *reinterpret_cast<const f32x4*>(&part[w][row][d]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += f * y[i];
+    // ---- join the waves
+    auto& part = lds->part;
+    auto &part_max = lds->part_max, &part_sum = lds->part_sum;
+    if (lane < kDecodeRows) {
+      part_max[wave][lane] = mref;
+      part_sum[wave][lane] = sum;
     }
-    if (parts == 1) {
-      T* dst = static_cast<T*>(p.out) + seq * p.o_ts + (head0 + row) * p.o_hs + d;
-      *reinterpret_cast<u32x2*>(dst) = finish<F>(o, total, p.v_scale);
-    } else {
-      store16_coherent(o, out_r, (uint32_t)(row * p.head_dim + d) * 4);
-      if (d == 0) {
-        store_shared(stats + 2 * row, m);
-        store_shared(stats + 2 * row + 1, total);
+    if (c < rows) {
+#pragma unroll
+      for (int j = 0; j < S::kVCols; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < S::kVDims; i += 4)
+            *reinterpret_cast<f32x4*>(&part[wave][c][j * 16 * S::kVDims + (4 * h + r) * S::kVDims + i]) =
+                f32x4{acc[j][i][r], acc[j][i + 1][r], acc[j][i + 2][r], acc[j][i + 3][r]};
+    }
+    __syncthreads();
+
+    const int quads = p.head_dim / 4;   // fp32 quadruples of a row
+    float* stats = p.stats + part_id * p.part_rows * 2;
+    const rsrc_t out_r = make_rsrc(p.partial + part_id * p.part_rows * p.head_dim, (uint32_t)(p.part_rows * p.head_dim * 4));
+    for (int x = threadIdx.x; x < rows * quads; x += 256) {
+      const int row = EXACT ? x / (DP / 4) : x / quads, d = 4 * (x - row * quads);
+      float m = part_max[0][row];
+#pragma unroll
+      for (int w = 1; w < kDecodeWaves; ++w) m = fmaxf(m, part_max[w][row]);
+      const float base = m == kNegInf ? 0.f : m;
+      float total = 0.f;
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kDecodeWaves; ++w) {
+        const float f = exp2_of(part_max[w][row] - base);
+        total += f * part_sum[w][row];
+        const f32x4 y = *reinterpret_cast<const f32x4*>(&part[w][row][d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += f * y[i];
+      }
+      if (parts == 1) {
+        T* dst = static_cast<T*>(p.out) + seq * p.o_ts + (head0 + row) * p.o_hs + d;
+        *reinterpret_cast<u32x2*>(dst) = finish<F>(o, total, p.v_scale);
+      } else {
+        store16_coherent(o, out_r, (uint32_t)(row * p.head_dim + d) * 4);
+        if (d == 0) {
+          store_shared(stats + 2 * row, m);
+          store_shared(stats + 2 * row + 1, total);
+        }
       }
     }
-  }
-  if (parts == 1) return;
-  if (!workgroup_arrive_last(p.counters + tile, (uint32_t)parts, &lds->flag)) return;
+    if (parts == 1) return;
+    if (!workgroup_arrive_last(p.counters + tile, (uint32_t)parts, &lds->flag)) return;
 
-  // ---- join the parts, in part order
-  join_parts<F>(p, tile, parts, rows, [&](int r) { return seq * p.o_ts + (head0 + r) * p.o_hs; });
+    // ---- join the parts, in part order
+    join_parts<F>(p, tile, parts, rows, [&](int r) { return seq * p.o_ts + (head0 + r) * p.o_hs; });
   }
 }
 

@@ -5,7 +5,10 @@ namespace qg {
 namespace {
 
 // A thread takes four outputs of a head at a time, `chunks` workgroups a sequence: its own
-// parts in order, then the shared ones.
+// parts in order, then the shared ones. A launch of its own rather than the last workgroup's
+// work: what a sequence's rows need comes from workgroups of both kinds. 64 sequences of 64
+// heads, 8 shared parts: 6.5 us for 20 MB of parts from the caches, most of it the launch and
+// the chain of length, group and parts.
 template <class F>
 __global__ void __launch_bounds__(256) attn_join_one(SharedArgs p, int chunks) {
   const uint32_t block = blockIdx.x + p.first_block;

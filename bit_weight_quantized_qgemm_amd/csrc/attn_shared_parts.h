@@ -7,6 +7,13 @@
 // the shared tokens' by the matrix units, with as many rows as the group has, the own tokens'
 // by the stream of the cache. The shared ones come first and are cut into about one
 // workgroup per compute unit, which leaves room for one of the others beside it.
+//
+// Measured on MI355X, us: 64 sequences on 8192 shared and up to 512 own tokens, 64/8 heads of
+// 128, bf16: both kinds 36, the join 6.5 (everything unshared: 201). The shared tokens alone
+// take 12.3 and 1.0 for each 64 of a part's tokens (16 here), which is start and end and the
+// matrix units; beside the own tokens' stream 8 more. With two shared workgroups to a unit no
+// own ones fit beside them: 57 in all. 128 sequences on 2048 and up to 256, 32/32 heads, fp16,
+// are bound by the own tokens' 272 MB: 62 and 5.
 #include "attn_decode.h"
 #include "attn_prefill.h"
 

@@ -4,7 +4,13 @@
 // Rows are sorted by adapter once per batch (lora_plan), so that a tile holds rows of
 // one adapter; then two launches per projection: A x (lora_shrink), and its product with
 // B, added to the base (lora_expand). A batch of single tokens is bound by the adapters'
-// bytes, prompts by x, base and out.
+// bytes, prompts by x, base and out. Measured on MI355X, us, both launches of a captured call
+// (floor: bytes at 5.13 TB/s, the rate of a large copy):
+//   1 row, 4096 to 4096, rank 16, fp16                                  8.8  (0.06)
+//   64 rows of 64 adapters, 8192 to 8192 + 1024 + 1024, rank 16, bf16  21.2  (14.6)
+//   128 rows of 24 adapters of ranks 8..64, 8192 to 28672, fp16        27.6  (13.2)
+//   1003 rows of 5 adapters, 4096 to 11008, rank 64, fp16              29.2  (12.1)
+//   8192 rows of 3 adapters, 8192 to 8192, rank 16, bf16               96.4  (78.8)
 #include "attn_device.h"
 #include "lora_internal.h"
 
@@ -19,7 +25,8 @@ constexpr int kPlanEach = (kMaxLoraAdapters + 1 + kPlanThreads - 1) / kPlanThrea
 // A counting sort by one workgroup: rows per adapter, their prefix sums (of rows and of
 // tiles), then every row to its place. Where rows of one adapter stand among each other
 // is left to the order of the LDS atomics: no output depends on it, since a row's sums
-// are its own whatever tile it is in.
+// are its own whatever tile it is in. One workgroup: the work is a few loads per row, and
+// it is done once for all projections of all layers (3.1 to 5.4 us).
 __global__ void __launch_bounds__(kPlanThreads) lora_plan(LoraPlanArgs p) {
   __shared__ int32_t count[kMaxLoraAdapters + 1], start[kMaxLoraAdapters + 1], first_tile[kMaxLoraAdapters + 1];
   __shared__ int32_t wave_rows[kPlanThreads / 64], wave_tiles[kPlanThreads / 64];
@@ -113,9 +120,14 @@ __device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int tile, int t
 // its columns, so that a lane ends with four ranks of one token; both operands go from
 // memory to registers as they stand. Rows and ranks that do not exist repeat the last
 // one's loads and are dropped at the end.
+//
+// Bound by memory, behind a chain of launch, plan entry, rows and first loads and before the
+// parts' join: 64 rows of 64 adapters at 48 ranks of 8192 take 12.3 us for 51 MB (4.1 TB/s),
+// 8192 rows of 8192 at rank 16 39 us for 134 MB, which a bare read takes in 22: without the
+// loads of x the latter took 10.6 us of then 39.8.
 template <class F, int RB, int NT>
 __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
-    constexpr int kUnroll = RB == 1 ? 4 : 2;
+  constexpr int kUnroll = RB == 1 ? 4 : 2;
   __shared__ __attribute__((aligned(16))) float part[kLoraWaves][RB * NT][64][4];
   __shared__ int flag;
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
@@ -275,11 +287,19 @@ __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
 // it), each with a product of its own. Ranks up to 16 leave half of a product's inner
 // length of 32 free: there the terms lie one after the other, against B twice (PAIRED),
 // and cost one product. KS: steps of 32 ranks.
+//
+// Bound by base, out and B: 8192 rows of 8192 columns at rank 16 take 55 us for 268 MB (4.9
+// TB/s, a copy's rate). Rows of B lie 2 * rank bytes apart, so where an adapter of rank 8 or
+// 16 lies in a pool of rank 64 its whole lines of 128 bytes are moved: 128 rows of 21 such
+// adapters on 28672 columns take 18 us for 14 MB of base and out and 77 MB of lines (counted
+// at the L2), of which the product uses 40.
 template <class F, int RB, int KS, bool PAIRED>
 __global__ void __launch_bounds__(256) lora_expand(LoraArgs p) {
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // workgroups that run together take the columns of the same rows
+  // workgroups that run together take the columns of the same rows (8192 rows, 8192 to 8192,
+  // rank 16, four tiles of columns to a wave: 61 us, 69 where they take the rows of the same
+  // columns)
   const uint32_t groups = p.group_begin[p.slices];
   const int tile_no = blockIdx.x / groups, group = blockIdx.x - tile_no * groups;
   const LoraTile t = RB == 1 ? lora_tile(p, tile_no, p.tiles16, 2) : lora_tile(p, tile_no, p.tiles64, 3);

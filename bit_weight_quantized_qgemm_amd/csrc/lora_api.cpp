@@ -168,7 +168,6 @@ int run_lora(const qgemm_lora_call& g) {
   a.tokens = (int32_t)g.num_tokens;
   a.adapters = w->num_adapters;
   a.k = (int32_t)w->K;
-  a.n = (int32_t)w->N;
   a.rank = w->rank;
   a.slices = w->slices;
   a.tiles16 = (int32_t)l.tiles16;

@@ -57,7 +57,7 @@ struct LoraArgs {
   uint32_t* counters;     // one per tile and chunk, zero between calls
   float* partial;         // [tile][chunk][split], in fragment order
   float* y;               // [sorted row][slices][rank_tiles * 16]
-  int32_t tokens, adapters, k, n, rank, slices;
+  int32_t tokens, adapters, k, rank, slices;
   int32_t tiles16, tiles64;   // word offsets of the tiles in the plan
   int32_t cap16, cap64;       // most tiles
   int32_t tall_a, tall_b;     // tiles of 64 rows for the first, the second product (0: of 16)
