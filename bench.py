@@ -36,6 +36,7 @@ from __future__ import annotations
 
 import argparse
 import ctypes
+import gc
 import json
 import math
 import os
@@ -557,6 +558,12 @@ def main():
         groups.setdefault(kernel_label(cs["plan"]), []).append(j)
     glist = list(groups.items())
     ev = lambda: torch.cuda.Event(enable_timing=True)
+    # Python collects its garbage when enough objects have been made, wherever that
+    # falls: a full collection (15 to 40 ms) between the warm-up and the timed steps
+    # leaves the GPU idle, and the start-of-load transient comes again (410-419
+    # instead of 453-457 TFLOP/s). So it is done before, and not until they end.
+    gc.collect()
+    gc.disable()
     wbounds = [[ev() for _ in glist] for _ in range(args.warmup)]
     w0 = ev()
     w0.record(stream)
@@ -591,6 +598,7 @@ def main():
     e1 = step_end[-1]
     torch.cuda.synchronize()
     wall = time.perf_counter() - t_wall
+    gc.enable()
     step_ms = e0.elapsed_time(e1) / args.steps
     step_flops = sum(alg_flops(c["M"], c["K"], c["N"]) for c in cases)
     value = step_flops / (step_ms * 1e-3) / 1e12
