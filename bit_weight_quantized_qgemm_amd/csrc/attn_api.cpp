@@ -479,7 +479,6 @@ int run_attn(const qgemm_attn_call& g, bool prefill, const Sharing* sharing) {
     a.shared_lens = sharing->shared_lens;
     a.num_groups = (int32_t)sharing->num_groups;
     a.max_shared = (int32_t)std::min(sharing->max_shared, g.max_len);
-    a.shared_row_tiles = (int32_t)(sp.tiles / c->kv_heads);
     a.shared_splits = sp.splits;
     a.shared_split_blocks = sp.split_blocks;
     a.split_step = prefill ? prefill_step(c->head_dim) : 2;   // decode: a pair of blocks

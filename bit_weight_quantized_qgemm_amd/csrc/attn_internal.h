@@ -79,7 +79,6 @@ struct SharedArgs : AttnArgs {
   float* shared_partial;    // [shared split][kv head][token][head of it][head_dim]
   float* shared_stats;      // [shared split][kv head][token][head of it] (maximum, sum)
   int32_t num_groups, max_shared;
-  int32_t shared_row_tiles; // tiles of 128 rows of a group, for each key-value head
   int32_t shared_splits;
   int32_t shared_split_blocks;   // token blocks of a part
   int32_t shared_blocks;    // workgroups of the shared tokens: the first ones of the launch
