@@ -1,0 +1,40 @@
+"""Attention over tokens that sequences share: joins of more rows than a launch has workgroups for at a time."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_weight_quantized_qgemm_amd as qg
+from attn_problem import check, to_bits, to_torch
+from oracle import attention as oa
+from shared_problem import SharedPaged
+from test_gpu_attn import DEV, PREFILL_WEIGHTS, _say, _values, _weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _modes():
+    qg.set_attn_splits(0)
+    qg.set_attn_sharing(1)
+    yield
+    qg.set_attn_splits(0)
+    qg.set_attn_sharing(0)
+
+
+@pytest.mark.parametrize("D,act,cache", [(80, "f16", "f16"), (128, "bf16", "fp8")])
+def test_joins_of_many_full_tiles(D, act, cache):
+    """From 1024 tiles of rows on a join's workgroups take several turns."""
+    _say("joins", D, act, cache)
+    rng = np.random.default_rng(D)
+    B, KV, new = 16, 32, 140   # 140 rows of a head: a full tile of 128 and one of 12
+    lens = [200 + 3 * i for i in range(B)]
+    pg = SharedPaged(rng, lens, [(B, 3, 48)], KV, D, cache, 16, DEV, scales=(2.0 ** -4, 2.0 ** -3) if cache == "fp8" else (1.0, 1.0))
+    T = B * new
+    bits, q = _values(rng, (T, KV, D), act)
+    start = torch.arange(0, T + 1, new, dtype=torch.int32, device=DEV)
+    out = qg.attn_prefill_shared(to_torch(bits, act, DEV), pg.cache, pg.table_dev, start, pg.lens_dev, new, max(lens),
+                                 pg.group_start, pg.shared_lens, pg.max_shared)
+    torch.cuda.synchronize()
+    refs = [pg.attend(t // new, q[t], lens[t // new] - new + t % new, D ** -0.5) for t in range(T)]
+    check(oa.decode(to_bits(out), act), refs, act, _weights(PREFILL_WEIGHTS, act, pg.fmt), D)
