@@ -284,11 +284,11 @@ __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
 // four waves of a workgroup columns next to each other. Columns are the rows of the
 // product and tokens its columns: row i of block j stands for column 32 (j / 2) + 8 (i / 4)
 // + 4 (j % 2) + i % 4, so that a lane ends with eight consecutive columns of one token
-// twice, and four lanes with 64 bytes. y is brought near 1 by a power of two per token and
-// goes in as two 16-bit terms (the rounded value and the rest, good to 2^-22 or 2^-16 of
-// it), each with a product of its own. Ranks up to 16 leave half of a product's inner
-// length of 32 free: there the terms lie one after the other, against B twice (PAIRED),
-// and cost one product. KS: steps of 32 ranks.
+// twice, and four lanes with 64 bytes. y is brought into range by a power of two per token
+// (fp16: near 1) and goes in as two 16-bit terms (the rounded value and the rest, good to
+// 2^-22 or 2^-16 of it), each with a product of its own. Ranks up to 16 leave half of a
+// product's inner length of 32 free: there the terms lie one after the other, against B
+// twice (PAIRED), and cost one product. KS: steps of 32 ranks.
 //
 // Bound by base, out and B: 8192 rows of 8192 columns at rank 16 take 55 us for 268 MB (4.9
 // TB/s, a copy's rate). Rows of B lie 2 * rank bytes apart, so where an adapter of rank 8 or
@@ -398,9 +398,13 @@ __global__ void __launch_bounds__(256, RB * KS == 1 ? 8 : 1) lora_expand(LoraArg
         for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[s][x][e]));
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // 2^e <= top < 2^(e+1) for normal values; an infinite or NaN sum stays what it is, the
-    // rest of an infinite one is 0
-    const int e = min(max((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127, -100), 100);
+    // 2^exponent <= top < 2^(exponent + 1) for normal values; an infinite or NaN sum stays what
+    // it is, the rest of an infinite one is 0. fp16 is brought near 1, as far as the factors are
+    // normal. bf16 has fp32's range, in which B times 1 may pass the end where B y does not: it
+    // stays as it is from 2^-60, whose rests are normal, to 2^-4, from which on B times 256
+    // rests could pass the end
+    const int exponent = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+    const int e = kHalf ? min(max(exponent, -100), 100) : exponent - min(max(exponent, -60), -4);
     const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
     if (h == 0) factors[b][c] = (p.scales ? p.scales[t.adapter] : 1.f) * __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
 #pragma unroll

@@ -1,5 +1,5 @@
-"""The low-rank adapters at the ends of their number formats: infinite second matrices. References are sums of products
-in 64 bits, in which infinities and NaN go their own way."""
+"""The low-rank adapters at the ends of their number formats: infinite second matrices, products of very large and very
+small values. References are sums of products in 64 bits, in which infinities and NaN go their own way."""
 
 import numpy as np
 import pytest
@@ -7,8 +7,9 @@ import torch
 
 import bit_weight_quantized_qgemm_amd as qg
 from attn_problem import to_bits, to_torch
-from lora_problem import values
+from lora_problem import check, values
 from oracle import attention as oa
+from oracle import lora as lora_oracle
 from test_gpu_lora import DEV, _batch, _say
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +65,42 @@ def test_infinite_second_matrices(T, rank, fmt):
     seen = odd & ~np.isnan(ref)
     assert np.isinf(ref[seen]).all() and np.array_equal(value[seen], ref[seen])
     assert np.array_equal(got[~odd], tame[~odd])
+
+
+@pytest.mark.parametrize("T", [7, 1100, 2570])
+@pytest.mark.parametrize("rank", [8, 16, 24, 72])
+@pytest.mark.parametrize("fmt,x_dev,a_dev,b", [("bf16", 1.0, 1e-3, 2e38), ("bf16", 1.0, 1e-9, 2e38), ("bf16", 1e18, 1e18, 1e-36),
+                                               ("bf16", 1e-18, 1e-18, 1e37), ("f16", 1.0, 1e-4, 4e4), ("f16", 1e3, 1e3, 1e-4)],
+                         ids=str)
+def test_values_at_the_ends_of_the_types(T, rank, fmt, x_dev, a_dev, b):
+    """A x and B near the ends of their type, with results of ordinary size or at least finite."""
+    _say("ends", T, rank, fmt, x_dev, a_dev, b)
+    rng = np.random.default_rng(rank + T)
+    n, K, N = 2, 40, 72
+    x_bits, x = values(rng, (T, K), fmt, x_dev)
+    a_bits, a = values(rng, (n, 1, rank, K), fmt, a_dev * K ** -0.5)
+    b_bits = oa.encode(b * rng.choice([-1.5, -1.0, 1.0, 1.5], (n, N, rank)) * (1.0 + 0.05 * rng.random((n, N, rank))), fmt)
+    ids = np.arange(T) % n
+    out = qg.lora(to_torch(x_bits, fmt, DEV), qg.LoraAdapters(to_torch(a_bits, fmt, DEV), to_torch(b_bits, fmt, DEV)),
+                  _batch(ids, n))
+    ref, bound = lora_oracle.lora(x, a, oa.decode(b_bits, fmt), ids, fmt)
+    assert np.abs(ref).max() < (60000 if fmt == "f16" else 1e38)
+    check(out, ref, bound, fmt, (T, rank, fmt, b))
+
+
+@pytest.mark.parametrize("T", [7, 1100, 2570])
+@pytest.mark.parametrize("rank", [8, 24, 256])
+def test_products_past_the_end_are_infinite(T, rank):
+    """Finite values of one sign whose product with B passes bf16's end, with rests of either sign."""
+    _say("past the end", T, rank)
+    rng = np.random.default_rng(rank + T)
+    n, K, N = 2, 24, 72
+    x_bits, x = values(rng, (T, K), "bf16", 1e16)
+    x_bits = oa.encode(np.abs(x) + 1e15, "bf16")
+    a_bits = oa.encode(1e10 * (1 + rng.random((n, 1, rank, K))), "bf16")
+    sign = rng.choice([-1.0, 1.0], (n, N, 1))
+    b_bits = oa.encode(sign * 1e38 * (1 + rng.random((n, N, rank))), "bf16")
+    ids = np.arange(T) % n
+    out = qg.lora(to_torch(x_bits, "bf16", DEV), qg.LoraAdapters(to_torch(a_bits, "bf16", DEV), to_torch(b_bits, "bf16", DEV)),
+                  _batch(ids, n))
+    assert np.array_equal(oa.decode(to_bits(out), "bf16"), (sign[ids, :, 0] * np.inf))
