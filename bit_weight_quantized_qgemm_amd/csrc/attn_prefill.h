@@ -188,8 +188,9 @@ template <PrefillMode MODE>
 using PrefillArgs = std::conditional_t<MODE == kAlone, AttnArgs, SharedArgs>;
 
 // DP: values of a head's place in LDS; DU: those that take part in the products. block:
-// workgroup among those of this kind.
-template <class F, class PF, bool FP8, int DP, int DU, bool EXACT, PrefillMode MODE>
+// workgroup among those of this kind. TWO: the weights go in as two 16-bit terms and are
+// summed unrounded, as in attn_decode.h.
+template <class F, class PF, bool FP8, int DP, int DU, bool EXACT, PrefillMode MODE, bool TWO = false>
 __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int block, char* lds) {
   using L = PrefillLds<DP>;
   using T = typename F::T;
@@ -479,14 +480,20 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
     }
   };
   // weights of 16 tokens (u = 0, 1 of a step's 32) as an operand
-  u32x4 w[2];
+  u32x4 w[2], rest[2];
   auto weigh = [&](const f32x16& s, int u) {
     const float base = weight_base<PF>(mref);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t x = PF::pack(exp2_of(__builtin_fmaf(s[8 * u + 2 * i], p.scale_log2, -base)),
-                                  exp2_of(__builtin_fmaf(s[8 * u + 2 * i + 1], p.scale_log2, -base)));
-      sum = PF::add_pair(x, sum);
+      const float e0 = exp2_of(__builtin_fmaf(s[8 * u + 2 * i], p.scale_log2, -base));
+      const float e1 = exp2_of(__builtin_fmaf(s[8 * u + 2 * i + 1], p.scale_log2, -base));
+      const uint32_t x = PF::pack(e0, e1);
+      if constexpr (TWO) {
+        sum += e0 + e1;
+        rest[u][i] = PF::pack(e0 - PF::lo(x), e1 - PF::hi(x));
+      } else {
+        sum = PF::add_pair(x, sum);
+      }
       w[u][i] = x;
     }
   };
@@ -522,6 +529,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
       if (i >= kSteps / 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
     }
     asm volatile("" : "+v"(w[0]));   // not moved past the masks
+    if constexpr (TWO) asm volatile("" : "+v"(rest[0]));
     __builtin_amdgcn_sched_barrier(0);
     if (more) mask(next, number + 1);
     __builtin_amdgcn_sched_barrier(0);
@@ -532,7 +540,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs<MODE>& p, int blo
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int d = 0; d < kDB; ++d) acc[d] = PF::mfma32(v[u][d], w[u], acc[d]);
+      for (int d = 0; d < kDB; ++d) {
+        acc[d] = PF::mfma32(v[u][d], w[u], acc[d]);
+        if constexpr (TWO) acc[d] = PF::mfma32(v[u][d], rest[u], acc[d]);
+      }
     const float top = largest(next);
 #pragma unroll
     for (int d = 0; d < kDB; ++d) {

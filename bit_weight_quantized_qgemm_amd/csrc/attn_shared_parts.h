@@ -9,11 +9,15 @@
 // workgroup per compute unit, which leaves room for one of the others beside it.
 //
 // Measured on MI355X, us: 64 sequences on 8192 shared and up to 512 own tokens, 64/8 heads of
-// 128, bf16: both kinds 36, the join 6.5 (everything unshared: 201). The shared tokens alone
+// 128, bf16: both kinds 41, the join 6.6 (everything unshared: 201). The shared tokens alone
 // take 12.3 and 1.0 for each 64 of a part's tokens (16 here), which is start and end and the
 // matrix units; beside the own tokens' stream 8 more. With two shared workgroups to a unit no
 // own ones fit beside them: 57 in all. 128 sequences on 2048 and up to 256, 32/32 heads, fp16,
-// are bound by the own tokens' 272 MB: 62 and 5.
+// are bound by the own tokens' 272 MB: 65 and 5.
+//
+// In a decode the shared tokens' weights have two 16-bit terms, as all have in the plain call.
+// With one, as in the many-token calls, the first case took 43 us instead of 48 and the other
+// 67 instead of 70, but the first was 2.3e-3 off 64 bits instead of its outputs' rounding, 1.7e-3.
 #include "attn_decode.h"
 #include "attn_prefill.h"
 
@@ -24,7 +28,7 @@ template <class F, class PF, bool FP8, int DP, int DU, bool EXACT, bool ONE>
 __global__ void __launch_bounds__(256, DP <= 128 ? 2 : 1) attn_parts(SharedArgs p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int block = blockIdx.x + p.first_block;
-  if (block < p.shared_blocks) prefill_body<F, PF, FP8, DP, DU, EXACT, kShared>(p, block, lds);
+  if (block < p.shared_blocks) prefill_body<F, PF, FP8, DP, DU, EXACT, kShared, ONE>(p, block, lds);
   else if constexpr (ONE)
     decode_body<F, PF, FP8, DP, EXACT, true>(
         p, (block - p.shared_blocks) * kDecodeWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nullptr);

@@ -510,7 +510,8 @@ int qgemm_attn_prefill_call(const qgemm_attn_call* call);
  * sizes grid and workspace), and up to 15 tokens of one, whose block is not whole, are read
  * for each sequence apart.
  *   - Keys and values of the tokens below shared_lens[g] have to be finite, seen or not.
- *   - The weights of shared tokens are rounded to one 16-bit term, as in prefill.
+ *   - The weights of all tokens have the terms of the plain call: two in a decode, one in a
+ *     prefill.
  *   - num_groups is 0..65535. Where the batch has less than two sequences per group the call
  *     is computed as if nothing were shared.
  * The struct is read before the call returns; attn holds what the plain call takes.

@@ -1,4 +1,5 @@
-"""Attention over tokens that sequences share: joins of more rows than a launch has workgroups for at a time."""
+"""Attention over tokens that sequences share: the accuracy of single tokens, which is the plain call's, and joins of more
+rows than a launch has workgroups for at a time."""
 
 import numpy as np
 import pytest
@@ -8,7 +9,8 @@ import bit_weight_quantized_qgemm_amd as qg
 from attn_problem import check, to_bits, to_torch
 from oracle import attention as oa
 from shared_problem import SharedPaged
-from test_gpu_attn import DEV, PREFILL_WEIGHTS, _say, _values, _weights
+from test_gpu_attn import DECODE_WEIGHTS, DEV, PREFILL_WEIGHTS, _say, _values, _weights
+from test_gpu_attn_shared import DECODE
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +22,22 @@ def _modes():
     yield
     qg.set_attn_splits(0)
     qg.set_attn_sharing(0)
+
+
+@pytest.mark.parametrize("splits", [0, 2])
+@pytest.mark.parametrize("lens,groups,before,H,KV,D,act,cache,page,layout,window,sinks", DECODE)
+def test_decode_weights_have_two_terms(lens, groups, before, H, KV, D, act, cache, page, layout, window, sinks, splits):
+    """The bound of attn_decode, whose weights enter the second product as two 16-bit terms, holds for shared tokens too."""
+    _say("decode weights", lens[:8], groups, before, H, KV, D, act, cache, page, layout, window, sinks, splits)
+    rng = np.random.default_rng(len(lens) + D + window + 1000)
+    scales = (2.0 ** -4, 2.0 ** -3) if cache == "fp8" else (1.0, 1.0)
+    pg = SharedPaged(rng, lens, groups, KV, D, cache, page, DEV, layout, scales, before)
+    qg.set_attn_splits(splits)
+    bits, q = _values(rng, (len(lens), H, D), act)
+    out = qg.attn_decode_shared(to_torch(bits, act, DEV), pg.cache, pg.table_dev, pg.lens_dev, max(lens), pg.group_start,
+                                pg.shared_lens, pg.max_shared, window=window, sinks=sinks)
+    refs = [pg.attend(b, q[b], n - 1, D ** -0.5, window, sinks) for b, n in enumerate(lens)]
+    check(oa.decode(to_bits(out), act), refs, act, _weights(DECODE_WEIGHTS, act, pg.fmt), (lens[:8], splits))
 
 
 @pytest.mark.parametrize("D,act,cache", [(80, "f16", "f16"), (128, "bf16", "fp8")])
