@@ -261,8 +261,11 @@ std::atomic<int> g_force_sharing{0};   // 1: always, 2: never
 
 // Sums of rows over shared tokens, next to those over own ones. Tiles of 128 rows are counted
 // as if the groups held them all and each began a tile (attn_shared.h). Own tokens: as many as
-// the longest context has past the longest shared run, as a guess; the kernel cuts each
-// sequence's own tokens into so many parts at most.
+// the longest context has past the longest shared run, as a guess. In a decode a sequence with
+// more of them (of no group, or of one with a shorter run) has them cut into more parts than
+// the others', up to what eight waves per compute unit give each (64 on 16384 and up to 64,
+// 64/8 heads, 81 us, with one more of 16384 own tokens 254; 2 of a group beside 6 of none 101.
+// In as many parts as the others' these took 874 and 864, the plain call 559 and 81).
 //
 // The shared tokens' workgroups stand beside the own ones', which are bound by the cache's
 // stream in a decode. Measured, us, by parts of the shared tokens:
@@ -294,6 +297,7 @@ qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, 
     const int64_t live = std::max(num_groups, (rows + qg::kPrefillRows - 1) / qg::kPrefillRows) * kv_heads;
     const int step = prefill_step(head_dim);
     double cost;
+    pl.own_parts = pl.own.splits;
     int64_t parts =
         prefill_parts(live, (int)std::min<int64_t>(rows, qg::kPrefillRows), blocks, head_dim, true, 1, &cost);
     const int64_t turns = (blocks + step - 1) / step;
@@ -311,8 +315,11 @@ qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, 
       cost += own_cost;
     } else {
       // a wave for each part: eight waves per compute unit, each with 128 tokens at least
-      const int64_t waves = 8 * cus, most = (visible_blocks(own_len, 1, own_mask) + 7) / 8;
-      pl.own.splits = (int)std::max<int64_t>(1, std::min((waves + pl.own.tiles - 1) / std::max<int64_t>(1, pl.own.tiles), most));
+      const int64_t tiles = std::max<int64_t>(1, pl.own.tiles), fill = (8 * cus + tiles - 1) / tiles;
+      const int64_t own = visible_blocks(own_len, 1, own_mask), all = std::max(own, visible_blocks(max_len, 1, mask));
+      pl.own_parts = (int)std::min(fill, std::max<int64_t>(1, (own + 7) / 8));
+      pl.own_part_blocks = (int)((own + pl.own_parts - 1) / pl.own_parts);
+      pl.own.splits = (int)std::min(fill, std::max<int64_t>(1, (all + 7) / 8));
       own_cost = value_mb * num_seqs * (mask.window ? std::min(own_len, mask.window + mask.sinks) : own_len) / 5.0;
       plain_cost = value_mb * num_seqs * (mask.window ? std::min(max_len, mask.window + mask.sinks) : max_len) / 6.0;
       // fewest parts that end with the own tokens, of which half are taken to be there
@@ -322,9 +329,9 @@ qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, 
       cost = std::max(own_cost, 2 * live <= cus ? turn * ((turns + parts - 1) / parts) : cost);
     }
     // start and end of the shared workgroups, the join's launch, and the parts that it reads
-    cost += 9 + 3 + 1e-6 * rows * q_heads / group * head_dim * 4 * (parts + pl.own.splits) / 4.0;
+    cost += 9 + 3 + 1e-6 * rows * q_heads / group * head_dim * 4 * (parts + pl.own_parts) / 4.0;
     pl.share = mode == 1 || cost < plain_cost + 4;
-    if (force) parts = pl.own.splits = force;
+    if (force) parts = pl.own_parts = pl.own.splits = force;
     const int64_t per = (blocks + parts - 1) / parts;
     pl.split_blocks = (int)((per + step - 1) / step * step);
     pl.splits = (int)((blocks + pl.split_blocks - 1) / pl.split_blocks);
@@ -482,6 +489,8 @@ int run_attn(const qgemm_attn_call& g, bool prefill, const Sharing* sharing) {
     a.shared_splits = sp.splits;
     a.shared_split_blocks = sp.split_blocks;
     a.split_step = prefill ? prefill_step(c->head_dim) : 2;   // decode: a pair of blocks
+    a.own_parts = sp.own_parts;
+    a.own_part_blocks = sp.own_part_blocks;
     a.inv_shared_splits = 1.0 / sp.splits;
     a.shared_blocks = (int32_t)(sp.tiles * sp.splits);
     e = prefill ? qg::launch_attn_prefill_shared(a, bf16, fp8, pl.tiles, s)

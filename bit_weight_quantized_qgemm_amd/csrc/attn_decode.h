@@ -95,7 +95,7 @@ __device__ __forceinline__ void decode_body(const std::conditional_t<OWN, Shared
   // never more than the workspace holds (the plan covers see.blocks with p.splits)
   int parts, split_blocks, v_first = 0;
   if constexpr (OWN) {
-    const OwnBlocks own = own_blocks(see, shared_tokens(p, seq), p.splits, p.split_step);
+    const OwnBlocks own = own_blocks(p, see, shared_tokens(p, seq));
     parts = own.parts;
     split_blocks = own.split_blocks;
     v_first = own.first;

@@ -83,6 +83,7 @@ struct SharedArgs : AttnArgs {
   int32_t shared_split_blocks;   // token blocks of a part
   int32_t shared_blocks;    // workgroups of the shared tokens: the first ones of the launch
   int32_t split_step;       // token blocks of an own part: a multiple of this
+  int32_t own_parts, own_part_blocks;   // of a sequence with the own tokens that the plan counts on
   double inv_shared_splits;
 };
 
@@ -120,6 +121,7 @@ struct AppendArgs {
 struct SharedPlan {
   AttnPlan own;
   bool share = false;       // false: computed as if nothing were shared
+  int own_parts = 1, own_part_blocks = 0;
   int64_t tiles = 0;        // of shared rows
   int splits = 1;
   int split_blocks = 1;

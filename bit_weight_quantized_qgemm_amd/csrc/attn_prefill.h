@@ -163,7 +163,7 @@ __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& p, int tile) {
 // The same tile without the tokens that its sequence shares.
 __device__ __forceinline__ RowTile own_tile_of(const SharedArgs& p, int tile) {
   RowTile rt = row_tile_of(p, tile);
-  const OwnBlocks own = own_blocks(rt.see, shared_tokens(p, rt.seq), p.splits, p.split_step);
+  const OwnBlocks own = own_blocks(p, rt.see, shared_tokens(p, rt.seq));
   rt.v_first = own.first;
   rt.split_blocks = own.split_blocks;
   rt.parts = own.parts;

@@ -140,17 +140,18 @@ __device__ __forceinline__ int position_of(const SharedArgs& p, int seq, int tok
   return i >= 0 && i < rows ? len - rows + i : -1;
 }
 
-// A sequence's virtual blocks past the tokens that it shares, in at most `splits` parts of
-// whole steps.
+// A sequence's virtual blocks past the tokens that it shares, in parts of whole steps: up to
+// own_parts parts, and where those would be longer than own_part_blocks (more own tokens than
+// the plan took the sequences to have) up to `splits`.
 struct OwnBlocks {
   int first, split_blocks, parts;
 };
-__device__ __forceinline__ OwnBlocks own_blocks(const Visible& see, int shared, int splits, int step) {
-  const int block = shared / kTokBlock;
+__device__ __forceinline__ OwnBlocks own_blocks(const SharedArgs& p, const Visible& see, int shared) {
+  const int block = shared / kTokBlock, step = p.split_step;
   OwnBlocks o;
   o.first = block <= see.sink_blocks ? block : max(see.sink_blocks, block - see.skip);
   const int blocks = max(0, see.blocks - o.first);
-  const int each = (blocks + splits - 1) / splits;
+  const int each = max((blocks + p.splits - 1) / p.splits, min((blocks + p.own_parts - 1) / p.own_parts, p.own_part_blocks));
   o.split_blocks = max(step, (each + step - 1) / step * step);
   o.parts = max(1, (blocks + o.split_blocks - 1) / o.split_blocks);
   return o;

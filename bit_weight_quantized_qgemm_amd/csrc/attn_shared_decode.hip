@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) attn_join_one(SharedArgs p, int chunks) {
   const int len = min(max(scalar_load(p.lens + seq), 0), p.max_len);
   const int shared = shared_tokens(p, seq);
   const Visible see(len, p.window ? len - p.window : 0, p.window ? p.sinks : 0);
-  const OwnBlocks own = own_blocks(see, shared, p.splits, p.split_step);
+  const OwnBlocks own = own_blocks(p, see, shared);
   const int quads = p.head_dim / 4, all = p.kv_heads * p.group * quads;
   for (int x = chunk * 256 + threadIdx.x; x < all; x += chunks * 256) {
     const int head = x / quads, d = 4 * (x - head * quads);

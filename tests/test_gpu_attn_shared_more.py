@@ -56,3 +56,23 @@ def test_joins_of_many_full_tiles(D, act, cache):
     torch.cuda.synchronize()
     refs = [pg.attend(t // new, q[t], lens[t // new] - new + t % new, D ** -0.5) for t in range(T)]
     check(oa.decode(to_bits(out), act), refs, act, _weights(PREFILL_WEIGHTS, act, pg.fmt), D)
+
+
+@pytest.mark.parametrize("lowered", [None, 0, 600])
+@pytest.mark.parametrize("act,cache,D,window,sinks", [("f16", "f16", 64, 0, 0), ("bf16", "fp8", 128, 0, 0), ("bf16", "bf16", 96, 500, 20),
+                                                      ("f16", "f16", 256, 0, 0)])
+def test_own_tokens_beyond_the_longest_context_less_the_shared_run(act, cache, D, window, sinks, lowered):
+    """Sequences of no group, and of one whose shared run is shorter than max_shared, have more own tokens than the plan
+    counts on, and more parts than the others."""
+    _say("long own runs", act, cache, D, window, sinks, lowered)
+    rng = np.random.default_rng(D + window)
+    scales = (2.0 ** -4, 2.0 ** -3) if cache == "fp8" else (1.0, 1.0)
+    lens = [1200, 1100, 1095, 1110, 1089, 1101, 700, 0, 1199, 300]
+    pg = SharedPaged(rng, lens, [(5, 68, 1088), (2, 20, 320)], 2, D, cache, 16, DEV, scales=scales, before=1)
+    if lowered is not None:
+        pg.shared_lens[0] = lowered
+    bits, q = _values(rng, (len(lens), 8, D), act)
+    out = qg.attn_decode_shared(to_torch(bits, act, DEV), pg.cache, pg.table_dev, pg.lens_dev, 1200, pg.group_start,
+                                pg.shared_lens, 1088, window=window, sinks=sinks)
+    refs = [pg.attend(b, q[b], n - 1, D ** -0.5, window, sinks) for b, n in enumerate(lens)]
+    check(oa.decode(to_bits(out), act), refs, act, _weights(DECODE_WEIGHTS, act, pg.fmt), (act, cache, D, lowered))
