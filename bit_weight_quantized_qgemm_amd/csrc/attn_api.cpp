@@ -261,11 +261,14 @@ std::atomic<int> g_force_sharing{0};   // 1: always, 2: never
 
 // Sums of rows over shared tokens, next to those over own ones. Tiles of 128 rows are counted
 // as if the groups held them all and each began a tile (attn_shared.h). Own tokens: as many as
-// the longest context has past the longest shared run, as a guess. In a decode a sequence with
-// more of them (of no group, or of one with a shorter run) has them cut into more parts than
-// the others', up to what eight waves per compute unit give each (64 on 16384 and up to 64,
-// 64/8 heads, 81 us, with one more of 16384 own tokens 254; 2 of a group beside 6 of none 101.
-// In as many parts as the others' these took 874 and 864, the plain call 559 and 81).
+// the longest context has past the longest shared run, as a guess. A sequence with more of them
+// (of no group, or of one with a shorter run) has them cut into more parts than the others': in
+// a decode up to what eight waves per compute unit give each, otherwise as many as the plain
+// call makes of the whole context. Measured with as many parts as the others' / so / plain, us:
+//  - decode, 64/8 heads: 64 on 16384 + 64 and one of 16384 own 874 / 254 / 559 (without that
+//    one 80 / 81); 2 of a group beside 6 of none 864 / 101 / 81.
+//  - 5 new tokens each, 64/8 heads: 16 on 6000 + 112 and one of 6000 own 134 / 56 / 69 (without
+//    that one 49.9 / 49.7); 2 of a group beside 6 of none, on 16384, 315 / 131 / 100.
 //
 // The shared tokens' workgroups stand beside the own ones', which are bound by the cache's
 // stream in a decode. Measured, us, by parts of the shared tokens:
@@ -305,7 +308,11 @@ qg::SharedPlan shared_plan(int64_t num_seqs, int64_t num_tokens, int64_t max_q, 
     if (2 * live <= cus) parts = std::min(cus / live, turns);
     double own_cost, plain_cost;
     if (prefill) {
-      const int64_t plain_blocks = visible_blocks(max_len, std::min<int64_t>(max_q, qg::kPrefillRows), mask);
+      const int64_t tile_q = std::min<int64_t>(max_q, qg::kPrefillRows), plain_blocks = visible_blocks(max_len, tile_q, mask);
+      // parts of more own tokens: as many as the plain call would make of them
+      const qg::AttnPlan plain = prefill_plan(num_seqs, max_q, max_len, q_heads, kv_heads, head_dim, mask);
+      pl.own_part_blocks = (int)((visible_blocks(own_len, tile_q, own_mask) + pl.own_parts - 1) / pl.own_parts);
+      pl.own.splits = std::max(pl.own_parts, plain.splits);
       // tiles that can hold rows: where few of the sequences are long, most of max_q's do not
       const int64_t own_live = std::min(pl.own.tiles, (rows / pl.own.part_rows + num_seqs) * kv_heads);
       prefill_parts(own_live, pl.own.part_rows, plain_blocks, head_dim, true, 1, &plain_cost);

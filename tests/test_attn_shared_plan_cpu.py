@@ -42,3 +42,15 @@ def test_parts_have_128_tokens_at_least():
 def test_a_window_bounds_the_parts():
     # 200 tokens of a window are in at most 15 blocks of 16 (both ends cut), two parts
     assert _parts(2, 16384 + 64, 16384, window=200) <= 256 // 8 + 2
+
+
+@pytest.mark.parametrize("seqs,new,KV,H", [(8, 16, 8, 64), (4, 32, 8, 64), (12, 10, 8, 64), (6, 16, 8, 64), (3, 32, 8, 64)])
+def test_several_tokens_of_a_sequence_of_no_group_have_the_plain_parts(seqs, new, KV, H):
+    """The same for several new tokens: own tokens have as many parts as the plain call makes of the whole context, next to
+    a part of the shared ones at least; those have at most one workgroup per unit in all."""
+    tokens, one, shared, bound = seqs * new, seqs * new * H * (128 + 2) * 4, 16384, 16384 + 64
+    plain = (qg.attn_prefill_workspace_bytes(seqs, new, bound, H, KV, 128) - 65536) // one
+    tiles = -(-tokens * H // KV // 128) * KV
+    assert plain > 256 // tiles
+    got = (qg.attn_prefill_shared_workspace_bytes(seqs, tokens, new, bound, H, KV, 128, 0, 0, 1, shared) - 65536) // one
+    assert plain + 1 <= got <= plain + 256 // tiles

@@ -76,3 +76,23 @@ def test_own_tokens_beyond_the_longest_context_less_the_shared_run(act, cache, D
                                 pg.shared_lens, 1088, window=window, sinks=sinks)
     refs = [pg.attend(b, q[b], n - 1, D ** -0.5, window, sinks) for b, n in enumerate(lens)]
     check(oa.decode(to_bits(out), act), refs, act, _weights(DECODE_WEIGHTS, act, pg.fmt), (act, cache, D, lowered))
+
+
+@pytest.mark.parametrize("act,cache,D,window,sinks", [("f16", "f16", 64, 0, 0), ("bf16", "fp8", 128, 0, 0), ("bf16", "bf16", 96, 500, 20),
+                                                      ("f16", "f16", 256, 0, 0)])
+def test_several_tokens_with_own_runs_beyond_the_plan(act, cache, D, window, sinks):
+    """As above for several new tokens, a sequence of none and one of more than a tile of rows among them."""
+    _say("long own runs, several tokens", act, cache, D, window, sinks)
+    rng = np.random.default_rng(D + window + 1)
+    scales = (2.0 ** -4, 2.0 ** -3) if cache == "fp8" else (1.0, 1.0)
+    lens = [1200, 1100, 1095, 1110, 1089, 1101, 700, 5, 1199, 300]
+    new = [3, 5, 2, 40, 1, 5, 5, 5, 2, 0]
+    pg = SharedPaged(rng, lens, [(5, 68, 1088), (2, 20, 320)], 2, D, cache, 16, DEV, scales=scales, before=1)
+    T, start = sum(new), np.concatenate([[0], np.cumsum(new)])
+    bits, q = _values(rng, (T, 8, D), act)
+    out = qg.attn_prefill_shared(to_torch(bits, act, DEV), pg.cache, pg.table_dev,
+                                 torch.tensor(start, dtype=torch.int32, device=DEV), pg.lens_dev, 40, 1200, pg.group_start,
+                                 pg.shared_lens, 1088, window=window, sinks=sinks)
+    refs = [pg.attend(b, q[start[b] + i], n - m + i, D ** -0.5, window, sinks) for b, (m, n) in enumerate(zip(new, lens))
+            for i in range(m)]
+    check(oa.decode(to_bits(out), act), refs, act, _weights(PREFILL_WEIGHTS, act, pg.fmt), (act, cache, D))
