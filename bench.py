@@ -20,7 +20,10 @@ every launch slowing by up to 35 % from about 3 ms after the load starts and
 recovering over the next 30 ms, after which the step time stays flat; the timed
 steps measure that steady state.
 
-Prints one JSON line. ``value`` is the aggregate TFLOP/s of the timed steps;
+Prints one JSON line of less than 4 KB, so that a reader who keeps only the end
+of the output has all of it; what else is measured (``secondary`` workloads,
+``context``, the plans and further figures of ``per_m``) goes to stderr before it, as
+``[bench] details`` and JSON. ``value`` is the aggregate TFLOP/s of the timed steps;
 ``per_m`` gives each launch's mean duration over a burst of back-to-back
 launches (HIP events around the burst), its TFLOP/s and roofline fractions;
 ``roofline`` describes the kernel with the largest share of a step (found in
@@ -113,6 +116,11 @@ def measured_traffic(label: str):
             kv = dict(x.split("=", 1) for x in l.split() if "=" in x)
             return float(kv["traffic_bytes_per_launch"])
     return None
+
+
+def short_row(row):
+    """What the printed line holds of a row of per_m."""
+    return {k: row[k] for k in ("shape", "M", "us", "tflops", "gbs", "hbm_frac", "mfma_frac")}
 
 
 def parse():
@@ -693,11 +701,10 @@ def main():
                    "weight_copies_rotated": len(cases[0]["blobs"]),
                    "wall_s_timed": round(wall, 3)},
         "roofline": roof,
-        "per_m": per_m,
+        "per_m": [short_row(r) for r in per_m],
         "cpu_baseline": cpu,
-        "secondary": sec,
-        "context": context,
     }
+    print("[bench] details " + json.dumps({"per_m": per_m, "secondary": sec, "context": context}), file=sys.stderr, flush=True)
     print(json.dumps(out), flush=True)
 
 
