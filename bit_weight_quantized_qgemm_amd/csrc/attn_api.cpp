@@ -272,13 +272,13 @@ std::atomic<int> g_force_sharing{0};   // 1: always, 2: never
 //
 // The shared tokens' workgroups stand beside the own ones', which are bound by the cache's
 // stream in a decode. Measured, us, by parts of the shared tokens:
-//  - 64 sequences on 8192 + 512, 64/8 heads, bf16 (32 tiles): 4 parts 55, 7 45, 8 46, 12 55:
+//  - 64 sequences on 8192 + 512, 64/8 heads, bf16 (32 tiles): 4 parts 63, 7 52, 8 51, 12 62:
 //    at most one workgroup per unit, since two leave no room for others.
-//  - 96 in 4 groups on 4096 + 700, 32/8, e4m3 (32 tiles): 2 parts 54, 4 36, 5 34, 8 39, 16 48.
-//  - 128 on 2048 + 256, 32/32, fp16 (128 tiles): 1 part 68, 2 71, 4 75, 8 83: no more parts
+//  - 96 in 4 groups on 4096 + 700, 32/8, e4m3 (32 tiles): 2 parts 62, 4 40, 5 37, 8 40, 16 47.
+//  - 128 on 2048 + 256, 32/32, fp16 (128 tiles): 1 part 71, 2 73, 4 76, 8 87: no more parts
 //    than end with the own tokens.
-// Own tokens of a decode, in waves of their own: the first case in 1, 2, 4 parts 53, 45, 46;
-// the second 50, 39, 38; the third 83, 82 in 1 and 2.
+// Own tokens of a decode, in waves of their own: the first case in 1, 2, 4 parts 55, 51, 51;
+// the second 43, 37, 37; the third 71, 71 in 1 and 2.
 // Where little is saved, everything is computed as in the plain call, by an estimate of both
 // (4 on 768 + 130, 32/32 heads: plain 13, shared 15; 24 prompts of up to 200 on 2048, 32/32
 // heads of 80: 121 and 116; 32 x 128 on 16384, 32/8, whose rows fill tiles by themselves: 1098

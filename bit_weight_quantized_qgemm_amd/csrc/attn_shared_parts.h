@@ -10,9 +10,9 @@
 //
 // Measured on MI355X, us: 64 sequences on 8192 shared and up to 512 own tokens, 64/8 heads of
 // 128, bf16: both kinds 41, the join 6.6 (everything unshared: 201). The shared tokens alone
-// take 12.3 and 1.0 for each 64 of a part's tokens (16 here), which is start and end and the
+// take 10.7 and 1.5 for each 64 of a part's tokens (16 here), which is start and end and the
 // matrix units; beside the own tokens' stream 8 more. With two shared workgroups to a unit no
-// own ones fit beside them: 57 in all. 128 sequences on 2048 and up to 256, 32/32 heads, fp16,
+// own ones fit beside them: 65 in all. 128 sequences on 2048 and up to 256, 32/32 heads, fp16,
 // are bound by the own tokens' 272 MB: 65 and 5.
 //
 // In a decode the shared tokens' weights have two 16-bit terms, as all have in the plain call.

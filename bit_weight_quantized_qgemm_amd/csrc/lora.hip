@@ -6,11 +6,11 @@
 // B, added to the base (lora_expand). A batch of single tokens is bound by the adapters'
 // bytes, prompts by x, base and out. Measured on MI355X, us, both launches of a captured call
 // (floor: bytes at 5.13 TB/s, the rate of a large copy):
-//   1 row, 4096 to 4096, rank 16, fp16                                  8.8  (0.06)
+//   1 row, 4096 to 4096, rank 16, fp16                                  9.1  (0.06)
 //   64 rows of 64 adapters, 8192 to 8192 + 1024 + 1024, rank 16, bf16  21.2  (14.6)
-//   128 rows of 24 adapters of ranks 8..64, 8192 to 28672, fp16        27.6  (13.2)
-//   1003 rows of 5 adapters, 4096 to 11008, rank 64, fp16              29.2  (12.1)
-//   8192 rows of 3 adapters, 8192 to 8192, rank 16, bf16               96.4  (78.8)
+//   128 rows of 24 adapters of ranks 8..64, 8192 to 28672, fp16        27.9  (13.2)
+//   1003 rows of 5 adapters, 4096 to 11008, rank 64, fp16              29.4  (12.1)
+//   8192 rows of 3 adapters, 8192 to 8192, rank 16, bf16               95.6  (78.8)
 #include "attn_device.h"
 #include "lora_internal.h"
 
@@ -28,7 +28,8 @@ constexpr int kPlanEach = (kMaxLoraAdapters + 1 + kPlanThreads - 1) / kPlanThrea
 // tiles), then every row to its place. Where rows of one adapter stand among each other
 // is left to the order of the LDS atomics: no output depends on it, since a row's sums
 // are its own whatever tile it is in. One workgroup: the work is a few loads per row, and
-// it is done once for all projections of all layers (3.1 to 5.4 us).
+// it is done once for all projections of all layers (3 to 5 us up to 1003 rows, 10 for 8192, 59
+// for 65535 of 4096 adapters).
 __global__ void __launch_bounds__(kPlanThreads) lora_plan(LoraPlanArgs p) {
   __shared__ int32_t count[kMaxLoraAdapters + 1], start[kMaxLoraAdapters + 1], first_tile[kMaxLoraAdapters + 1];
   __shared__ int32_t wave_rows[kPlanThreads / 64], wave_tiles[kPlanThreads / 64];
