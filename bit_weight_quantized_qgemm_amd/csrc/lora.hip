@@ -19,8 +19,6 @@
 namespace qg {
 namespace {
 
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanEach = (kMaxLoraAdapters + 1 + kPlanThreads - 1) / kPlanThreads;   // adapters per thread
 
@@ -298,17 +296,18 @@ __global__ void __launch_bounds__(256) lora_shrink(LoraArgs p) {
 // at the L2), of which the product uses 40.
 //
 // An infinite value of B times a rest of 0, or of the other sign than its first term, would
-// make NaN of a sum that is infinite. So a value that is not 0 has a first term that is not
-// (the smallest normal one, less which the rest then is), and where a sum comes out NaN it
-// is computed again with the infinities of B left out of the rests' products (behind the
-// stores: 64 rows of 64 adapters 20.1 us a call, 19.9 without the look, other cases the same;
-// between products and stores 128 rows on 28672 columns took 28.5 instead of 27.5). Eight
-// waves per SIMD are asked for where six would be left (64 rows 20.5).
+// make NaN of a sum that is infinite, and so would a rest's product that passes the end beside
+// a first term's. So a value that is not 0 has a first term that is not (the smallest normal
+// one, less which the rest then is), and a sum that comes out NaN is taken from the first terms
+// alone, which are infinite, or NaN, where the formula is (behind the stores: 64 rows of 64
+// adapters 20.0 us a call, 19.8 without the look, other cases the same; between products and
+// stores 128 rows on 28672 columns took 28.5 instead of 27.5). The launch bounds keep the waves
+// that this would cost (128 rows 30.2 with four per SIMD instead of five, 64 rows 20.5 with
+// six instead of eight).
 template <class F, int RB, int KS, bool PAIRED>
-__global__ void __launch_bounds__(256, RB * KS == 1 ? 8 : 1) lora_expand(LoraArgs p) {
+__global__ void __launch_bounds__(256, KS > 2 ? 1 : RB == 1 ? (KS == 1 ? 8 : 5) : (KS == 1 ? 4 : 3)) lora_expand(LoraArgs p) {
   constexpr bool kHalf = std::is_same_v<F, F16>;
   constexpr uint32_t kSmallest = kHalf ? 0x0400u : 0x0080u;   // normal value
-  constexpr uint16_t kLargest = kHalf ? 0x7BFF : 0x7F7F;      // finite value
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroups that run together take the columns of the same rows (8192 rows, 8192 to 8192,
@@ -402,10 +401,9 @@ __global__ void __launch_bounds__(256, RB * KS == 1 ? 8 : 1) lora_expand(LoraArg
     // 2^exponent <= top < 2^(exponent + 1) for normal values; an infinite or NaN sum stays what
     // it is, the rest of an infinite one is 0. fp16 is brought near 1, as far as the factors are
     // normal. bf16 has fp32's range, in which B times 1 may pass the end where B y does not: it
-    // stays as it is from 2^-60, whose rests are normal, to 2^-4, from which on B times 256
-    // rests could pass the end
+    // stays as it is between 2^-60, whose rests are normal, and 2^120, whose first terms are finite
     const int exponent = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
-    const int e = kHalf ? min(max(exponent, -100), 100) : exponent - min(max(exponent, -60), -4);
+    const int e = kHalf ? min(max(exponent, -100), 100) : exponent - min(max(exponent, -60), 119);
     const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
     if (h == 0) factors[b][c] = (p.scales ? p.scales[t.adapter] : 1.f) * __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
 #pragma unroll
@@ -433,9 +431,8 @@ __global__ void __launch_bounds__(256, RB * KS == 1 ? 8 : 1) lora_expand(LoraArg
   __syncthreads();
   if (!mine) return;
 
-  // ---- columns; rest: B as it meets the second terms (PAIRED: in lanes h >= eights). True where
-  // a sum is NaN.
-  auto columns = [&](const auto& rest) {
+  // ---- columns; true where a sum is NaN. again: such sums from the first terms alone
+  auto columns = [&](auto again) {
     bool nan = false;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
@@ -448,10 +445,23 @@ __global__ void __launch_bounds__(256, RB * KS == 1 ? 8 : 1) lora_expand(LoraArg
           if (4 * s < eights) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              acc[j] = F::mfma16(PAIRED ? rest(w[j][s]) : w[j][s], terms[b][s][0][lane], acc[j]);
-              if constexpr (!PAIRED) acc[j] = F::mfma16(rest(w[j][s]), terms[b][s][1][lane], acc[j]);
+              acc[j] = F::mfma16(w[j][s], terms[b][s][0][lane], acc[j]);
+              if constexpr (!PAIRED) acc[j] = F::mfma16(w[j][s], terms[b][s][1][lane], acc[j]);
             }
           }
+        if constexpr (decltype(again)::value) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f32x4 first = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s)   // PAIRED: lanes h >= eights hold rests
+              if (4 * s < eights)
+                first = F::mfma16(!PAIRED || h < eights ? w[j][s] : u32x4{0, 0, 0, 0}, terms[b][s][0][lane], first);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (acc[j][i] != acc[j][i]) acc[j][i] = first[i];
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -475,17 +485,7 @@ __global__ void __launch_bounds__(256, RB * KS == 1 ? 8 : 1) lora_expand(LoraArg
     return nan;
   };
   for (;;) {
-    if (__builtin_expect(__any(columns([](u32x4 x) { return x; })), 0)) {
-      const uint16_t most = PAIRED && h < eights ? 0x7FFF : kLargest;
-      columns([&](u32x4 x) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const u16x2 size = __builtin_elementwise_min(__builtin_bit_cast(u16x2, x[i] & 0x7FFF7FFFu), u16x2{most, most});
-          x[i] = (x[i] & 0x80008000u) | __builtin_bit_cast(uint32_t, size);
-        }
-        return x;
-      });
-    }
+    if (__builtin_expect(__any(columns(std::false_type())), 0)) columns(std::true_type());
     col += kLoraWaves * kLoraCols;
     const bool more = col < group_end;
     if (more) {

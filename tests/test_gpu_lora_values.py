@@ -104,3 +104,30 @@ def test_products_past_the_end_are_infinite(T, rank):
     out = qg.lora(to_torch(x_bits, "bf16", DEV), qg.LoraAdapters(to_torch(a_bits, "bf16", DEV), to_torch(b_bits, "bf16", DEV)),
                   _batch(ids, n))
     assert np.array_equal(oa.decode(to_bits(out), "bf16"), (sign[ids, :, 0] * np.inf))
+
+
+@pytest.mark.parametrize("T", [7, 1100, 2570])
+@pytest.mark.parametrize("rank", [8, 16, 24, 72])
+def test_sums_near_the_end_of_fp32(T, rank):
+    """A x of 1e36 to 1e38, a few powers of two below what fp32 holds, beside ranks of ordinary size; columns of B
+    that are 0 stay 0."""
+    _say("sums near the end", T, rank)
+    rng = np.random.default_rng(rank + T)
+    n, K, N = 2, 40, 72
+    x_bits, x = values(rng, (T, K), "bf16", 5e18)
+    a_bits, a = values(rng, (n, 1, rank, K), "bf16", 5e18 * K ** -0.5)
+    small = oa.encode(a * np.where(np.arange(rank) % 4 == 1, 2.0 ** -120, 1.0)[:, None], "bf16")   # ranks 1, 5, ..
+    small[:, :, 2::4] = oa.encode(a[:, :, 2::4] * 2.0 ** -24, "bf16")
+    a = oa.decode(small, "bf16")
+    b_bits, b = values(rng, (n, N, rank), "bf16", 1e-37)
+    b_bits[:, ::8] = 0
+    b = oa.decode(b_bits, "bf16")
+    ids = np.arange(T) % n
+    scales = torch.tensor([1.0, -300.0], device=DEV)
+    out = qg.lora(to_torch(x_bits, "bf16", DEV), qg.LoraAdapters(to_torch(small, "bf16", DEV), to_torch(b_bits, "bf16", DEV),
+                                                                scales=scales), _batch(ids, n))
+    y = np.einsum("trk,tk->tr", a[ids, 0], x)
+    assert 2.0 ** 124 < np.abs(y).max() < 3e38
+    ref, bound = lora_oracle.lora(x, a, b, ids, "bf16", scales=scales.cpu().numpy())
+    check(out, ref, bound, "bf16", (T, rank))
+    assert not (to_bits(out)[:, ::8] & 0x7FFF).any()
