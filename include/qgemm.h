@@ -597,7 +597,8 @@ int qgemm_lora_plan(const int32_t* ids, int64_t num_tokens, int64_t num_adapters
  * adapters->num_adapters must be those of the plan (with a plan of others nothing is
  * written). A x is summed in fp32, goes on as two 16-bit terms (good to 2^-22 of the
  * row's largest, bf16 2^-16) and its product with B is summed in fp32; each output is
- * rounded once. Infinities and NaN of any operand come out as the formula makes of them. Other rows and the order of the ids have no influence on a row: its result
+ * rounded once. Infinities and NaN of any operand come out as the formula makes of
+ * them. Other rows and the order of the ids have no influence on a row: its result
  * depends on its own values and adapter and on the numbers of the call, and does not change
  * from run to run. The workspace (always needed) follows qgemm_workspace_bytes' contract.
  */
